@@ -101,7 +101,7 @@ typedef enum { MUON_KIND_MUON = 0, MUON_KIND_ADAMW = 1 } muon_kind_t;
 /* One parameter tensor.  For kind MUON: a hidden weight matrix.  For kind
  * ADAMW: any parameter viewed as rows x cols (a vector as 1 x n); momentum
  * holds AdamW's first moment and exp_avg_sq its second (both float32, same
- * leading dimension ld_momentum); split_rows, precond and update_out must be
+ * leading dimension ld_momentum; or both packed in 8 bits); split_rows, precond and update_out must be
  * 0, -1 and NULL. */
 typedef struct {
   void* param;          /* rows x cols, dtype; updated in place               */
@@ -119,7 +119,12 @@ typedef struct {
                            cols); receives the orthogonalised update O of this
                            step, before lr/scale.  NULL = not written.        */
   int32_t kind;         /* muon_kind_t; 0 (MUON) in a zero-filled struct      */
-  int32_t reserved;     /* 0                                                  */
+  union {
+    int32_t state_bits; /* kind ADAMW: bits a moment's element is held in: 0 or
+                           32 float32, 8 packed (see "Packed moments" below);
+                           kind MUON: 0 or 32                                 */
+    int32_t reserved;   /* the field's former name                            */
+  };
   float* exp_avg_sq;    /* kind ADAMW: rows x cols float32 second moment,
                            leading dimension ld_momentum; NULL for MUON       */
 } muon_tensor_t;
@@ -251,6 +256,67 @@ const char* muon_phase_name(muon_handle_t h, int32_t phase);
  * value. */
 muon_status_t muon_set_adam_step(muon_handle_t h, int64_t steps_taken, void* stream);
 muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_taken);
+
+/* Packed moments: AdamW's moments in one byte an element (state_bits = 8).
+ *
+ * momentum and exp_avg_sq then each point to a buffer of
+ * muon_packed_moment_bytes(rows * cols) bytes, 16-byte aligned, with
+ * ld_momentum = cols; param and grad keep their leading dimensions.  A buffer
+ * holds the bytes of the row-major elements, filled up to whole blocks of 256,
+ * then a 16-bit scale for each block.  A zero-filled buffer holds zeros.
+ *   first moment   e4m3 number * 2^(e-127), e the block's scale: within 1/16
+ *                  of the value down to 2^-14 of the block's largest, then
+ *                  within 2^-18 of the largest (distances of neighbours are
+ *                  twice that)
+ *   second moment  the float32 with the bits (byte + scale) << 20, zero for
+ *                  byte 0: 8 values a binade over 31 binades below the block's
+ *                  largest; smaller ones are raised to the smallest value, and
+ *                  only zero is held as zero, so that no m / sqrt(v) is blown up
+ * A step computes both moments in float32, updates the weight with them as
+ * computed, and then rounds them up or down at random so that the mean is the
+ * value itself: rounded to nearest, a moment whose change is less than half
+ * the distance of two values would stay where it is.  The random bits are a
+ * function of (seed, step count, place of the tensor in the list, element), so
+ * equal runs give equal bytes, also from a replayed graph.  The noise this adds
+ * to a moment is about 0.04 / sqrt(1 - beta^2) of it: 8 % of the first moment at
+ * beta1 = 0.9, 12 % of the second at beta2 = 0.95 (6 % of its root), but 26 % at
+ * beta2 = 0.99 and over 80 % at 0.999: take float32 moments there.
+ * A first moment that is not finite stays so (NaN) and sets flag bit 0; the
+ * other elements of its block are not affected.
+ *
+ * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35. */
+size_t muon_packed_moment_bytes(int64_t n);
+
+/* Seed of the random rounding (0 until set); host only, from the next
+ * muon_step on (a captured step keeps the seed it was captured with). */
+muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed);
+
+/* Converts every packed moment of the handle from or to plain values, one
+ * launch, asynchronous on `stream` (checkpoints; a run that changes between
+ * float32 and packed moments).  `values` (dtype float32 or bf16, device
+ * memory, apart from the registered tensors and the workspace): with N the
+ * elements of all tensors with state_bits 8, first N first moments, tensor
+ * after tensor in the order of the list, then N second moments.  Packing
+ * rounds to nearest, ties to even (a second moment that is negative or NaN
+ * makes the first one NaN, and non-finite first moments set flag bit 0);
+ * unpacking is exact in both dtypes.  Without packed tensors both do nothing
+ * and `values` may be NULL. */
+muon_status_t muon_pack_moments(muon_handle_t h, const void* values, int32_t dtype, void* stream);
+muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, void* stream);
+
+/* Clipping by the global norm: with max_norm > 0 every following muon_step
+ * computes norm = sqrt(sum of the squares of every registered gradient, Muon
+ * and AdamW) in float64 and multiplies each gradient by
+ * min(1, max_norm / norm) as it reads it; the gradients in memory stay as they
+ * are.  INFINITY measures without clipping, 0 (the default) switches both off.
+ * A gradient that is not finite makes the norm so, and with it the factor: NaN
+ * for NaN, 0 for an infinite norm (whose infinite gradients become NaN).
+ * norm_out: NULL, or device memory for two floats that each step fills with
+ * (norm, factor) on its stream; it must live as long as it is set.  Host only;
+ * a captured step keeps what was set when it was captured.  A handle of
+ * muon_init_static whose request fills the static scratch up to the last few
+ * kilobytes returns MUON_ERR_WORKSPACE_TOO_SMALL. */
+muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* norm_out);
 
 /* Synchronises `stream` and returns the sticky flag word:
  * bit 0 = a non-finite value was seen in an update, bit 1 = a

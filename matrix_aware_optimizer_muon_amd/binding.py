@@ -7,6 +7,7 @@ or cannot be loaded, every entry point raises: there is no CPU fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import json
 import os
@@ -36,8 +37,17 @@ class MuonTensor(ctypes.Structure):
         ("ld_param", ctypes.c_int64), ("ld_grad", ctypes.c_int64), ("ld_momentum", ctypes.c_int64),
         ("dtype", ctypes.c_int32), ("split_rows", ctypes.c_int32), ("precond", ctypes.c_int32),
         ("lr_mult", ctypes.c_float), ("update_out", ctypes.c_void_p),
-        ("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("exp_avg_sq", ctypes.c_void_p),
+        ("kind", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("exp_avg_sq", ctypes.c_void_p),
     ]
+
+    @property
+    def reserved(self):
+        """The former name of state_bits."""
+        return self.state_bits
+
+    @reserved.setter
+    def reserved(self, v):
+        self.state_bits = v
 
 
 class MuonPrecond(ctypes.Structure):
@@ -100,6 +110,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_get_flags": (i32, [vp, vp, i32, ctypes.POINTER(ctypes.c_uint32)]),
         "muon_set_adam_step": (i32, [vp, i64, vp]),
         "muon_get_adam_step": (i32, [vp, vp, ctypes.POINTER(i64)]),
+        "muon_packed_moment_bytes": (sz, [i64]),
+        "muon_set_rounding_seed": (i32, [vp, ctypes.c_uint64]),
+        "muon_set_max_grad_norm": (i32, [vp, f32, vp]),
+        "muon_pack_moments": (i32, [vp, vp, i32, vp]),
+        "muon_unpack_moments": (i32, [vp, vp, i32, vp]),
         "muon_destroy": (i32, [vp]),
         "muon_plan_describe": (i32, [PT, i32, PP, i32, PH, ctypes.c_char_p, sz, ctypes.POINTER(sz)]),
         "muon_status_str": (ctypes.c_char_p, [i32]),
@@ -229,20 +244,72 @@ def tensor_desc(param, grad, momentum, *, split_rows=0, precond=-1, lr_mult=1.0,
     return d
 
 
+def packed_moment_bytes(n: int) -> int:
+    """Bytes of one packed moment of a parameter with n elements."""
+    b = load_library().muon_packed_moment_bytes(n)
+    if b == 0:
+        raise ValueError("a packed moment has 1 to 2**35 elements")
+    return b
+
+
+def packed_moment(param):
+    """A packed (8-bit) AdamW moment for `param`, holding zeros: pass two of
+    them to adam_tensor_desc in place of the float32 moments."""
+    return _torch().zeros(packed_moment_bytes(param.numel()), dtype=_torch().uint8, device=param.device)
+
+
+def _adam_matrix(t):
+    """An AdamW tensor as rows x cols: a vector as 1 x n, a >= 2-D tensor as
+    shape[0] x rest."""
+    if t.dim() == 1:
+        return t.view(1, -1) if t.is_contiguous() else t.unsqueeze(0)
+    return _as_matrix(t)
+
+
+def _packed_adam_desc(param, grad, exp_avg, exp_avg_sq, lr_mult) -> MuonTensor:
+    torch = _torch()
+    if grad.shape != param.shape:
+        raise ValueError("param and grad must share one shape")
+    if param.dtype != grad.dtype:
+        raise ValueError("param and grad must share a dtype")
+    for t in (exp_avg, exp_avg_sq):
+        if t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous() \
+                or t.numel() != packed_moment_bytes(param.numel()):
+            raise ValueError("packed moments are two contiguous uint8 vectors of "
+                             "packed_moment_bytes(param.numel()) bytes")
+    if not (param.device == grad.device == exp_avg.device == exp_avg_sq.device):
+        raise ValueError("param, grad and moments must be on one device")
+    param, grad = _adam_matrix(param), _adam_matrix(grad)
+    for t in (param, grad):
+        if t.stride(1) != 1:
+            raise ValueError("tensors must be row-major (unit column stride)")
+    dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(param.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {param.dtype}")
+    d = MuonTensor()
+    d.param, d.grad = param.data_ptr(), grad.data_ptr()
+    d.momentum, d.exp_avg_sq = exp_avg.data_ptr(), exp_avg_sq.data_ptr()
+    d.rows, d.cols = param.shape
+    d.ld_param, d.ld_grad, d.ld_momentum = param.stride(0), grad.stride(0), d.cols
+    d.dtype, d.split_rows, d.precond, d.lr_mult = dt, 0, -1, lr_mult
+    d.kind, d.state_bits = KIND_ADAMW, 8
+    d.update_out = None
+    return d
+
+
 def adam_tensor_desc(param, grad, exp_avg, exp_avg_sq, *, lr_mult=1.0) -> MuonTensor:
     """A parameter stepped with AdamW (embedding, head, gain, bias): any
     shape, viewed as rows x cols (a vector as 1 x n, a >= 2-D tensor as
-    shape[0] x rest); exp_avg and exp_avg_sq are its float32 moments."""
+    shape[0] x rest); exp_avg and exp_avg_sq are its moments, float32 of the
+    parameter's shape or packed in 8 bits (packed_moment)."""
     torch = _torch()
+    if exp_avg.dtype == torch.uint8 or exp_avg_sq.dtype == torch.uint8:
+        return _packed_adam_desc(param, grad, exp_avg, exp_avg_sq, lr_mult)
     if not (grad.shape == param.shape == exp_avg.shape == exp_avg_sq.shape):
         raise ValueError("param, grad and both moments must share one shape")
     if exp_avg.stride() != exp_avg_sq.stride():
         raise ValueError("the two moments must share one layout")
-    if param.dim() == 1:
-        param, grad, exp_avg, exp_avg_sq = (t.view(1, -1) if t.is_contiguous() else t.unsqueeze(0)
-                                            for t in (param, grad, exp_avg, exp_avg_sq))
-    else:
-        param, grad, exp_avg, exp_avg_sq = (_as_matrix(t) for t in (param, grad, exp_avg, exp_avg_sq))
+    param, grad, exp_avg, exp_avg_sq = (_adam_matrix(t) for t in (param, grad, exp_avg, exp_avg_sq))
     for t in (param, grad, exp_avg, exp_avg_sq):
         if t.stride(1) != 1:
             raise ValueError("tensors must be row-major (unit column stride)")
@@ -287,18 +354,22 @@ class MuonStep:
         self._pcs, self._npc = _array(list(preconds), MuonPrecond)
         self.workspace_bytes = workspace_size(descs, self.hp, preconds, lib=self._lib)
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self._keep = list(keepalive)
+        self.grad_norm = None
         h = ctypes.c_void_p()
         if static_scratch:
             self.workspace = None
-            with torch.cuda.device(self.device):
+            with self._here():
                 self._check(self._lib.muon_init_static(ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
                                                   ctypes.byref(self.hp), self._stream(None)))
         else:
             self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
-            self._check(self._lib.muon_init(ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
-                                       ctypes.byref(self.hp), ctypes.c_void_p(self.workspace.data_ptr()),
-                                       self.workspace.numel(), self._stream(None)))
+            with self._here():
+                self._check(self._lib.muon_init(ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
+                                           ctypes.byref(self.hp), ctypes.c_void_p(self.workspace.data_ptr()),
+                                           self.workspace.numel(), self._stream(None)))
         self._h = h
 
     def _torch_stream(self, stream):
@@ -307,6 +378,13 @@ class MuonStep:
 
     def _stream(self, stream):
         return ctypes.c_void_p(self._torch_stream(stream).cuda_stream)
+
+    def _here(self):
+        """The handle's device as the current one, for a call that launches
+        kernels (HIP launches on the current device)."""
+        torch = _torch()
+        return contextlib.nullcontext() if torch.cuda.current_device() == self.device.index \
+            else torch.cuda.device(self.device)
 
     @staticmethod
     def _guard(acts, stream):
@@ -328,7 +406,8 @@ class MuonStep:
         _check(status, self._lib)
 
     def step(self, lr: float = -1.0, stream=None):
-        self._check(self._lib.muon_step(self._h, ctypes.c_float(lr), self._stream(stream)))
+        with self._here():
+            self._check(self._lib.muon_step(self._h, ctypes.c_float(lr), self._stream(stream)))
 
     def step_timed(self, lr: float = -1.0, stream=None):
         """Run one step with HIP events between launches; returns
@@ -373,6 +452,78 @@ class MuonStep:
         """Rebuild S^-1 of (slot, block) from its running second moment."""
         self._check(self._lib.muon_precond_refresh_accumulated(self._h, slot, block, ctypes.c_float(damping),
                                                           int(reset), self._stream(stream)))
+
+    def set_rounding_seed(self, seed: int):
+        """Seed of the random rounding of packed moments (0 until set)."""
+        self._check(self._lib.muon_set_rounding_seed(self._h, int(seed) & (2 ** 64 - 1)))
+
+    def set_max_grad_norm(self, max_norm: float):
+        """Clip by the global norm of all registered gradients in every
+        following step (float('inf'): measure only; 0: off).  `grad_norm` is
+        then a device tensor that each step fills with (norm, factor); it is
+        None while off."""
+        torch = _torch()
+        out = None
+        if max_norm > 0:
+            out = self.grad_norm if self.grad_norm is not None else torch.zeros(2, device=self.device)
+        self._check(self._lib.muon_set_max_grad_norm(self._h, ctypes.c_float(max_norm),
+                                                ctypes.c_void_p(out.data_ptr() if out is not None else None)))
+        self.grad_norm = out
+
+    def packed_elements(self) -> int:
+        """Elements of all tensors with packed moments."""
+        return sum(d.rows * d.cols for d in self._descs[:self._n] if d.kind == KIND_ADAMW and d.state_bits == 8)
+
+    def pack_moments(self, values, stream=None):
+        """Set every packed moment from `values`, a contiguous float32 or
+        bfloat16 tensor [2, packed_elements()]: the first moments of all packed
+        tensors one after another, then the second ones (round to nearest)."""
+        torch = _torch()
+        n = self.packed_elements()
+        if tuple(values.shape) != (2, n) or not values.is_contiguous() or values.device != self.device:
+            raise ValueError(f"values must be a contiguous tensor of shape (2, {n}) on {self.device}")
+        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(values.dtype)
+        if dt is None:
+            raise ValueError(f"unsupported dtype {values.dtype}")
+        s = self._torch_stream(stream)
+        with self._here():
+            self._check(self._lib.muon_pack_moments(self._h, ctypes.c_void_p(values.data_ptr()), dt,
+                                               ctypes.c_void_p(s.cuda_stream)))
+        self._guard(values, s)
+
+    def unpack_moments(self, dtype=None, out=None, stream=None):
+        """The values of every packed moment, exactly, as a tensor
+        [2, packed_elements()] of `dtype` (float32 or bfloat16; default
+        float32), laid out as pack_moments takes it; into `out` if given.
+        split_moments cuts it into the tensors' own."""
+        torch = _torch()
+        n = self.packed_elements()
+        if out is None:
+            out = torch.empty(2, n, dtype=dtype or torch.float32, device=self.device)
+        elif tuple(out.shape) != (2, n) or not out.is_contiguous() or out.device != self.device \
+                or (dtype is not None and dtype != out.dtype):
+            raise ValueError(f"out must be a contiguous tensor of shape (2, {n}) on {self.device}, of dtype if given")
+        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(out.dtype)
+        if dt is None:
+            raise ValueError(f"unsupported dtype {out.dtype}")
+        s = self._torch_stream(stream)
+        with self._here():
+            self._check(self._lib.muon_unpack_moments(self._h, ctypes.c_void_p(out.data_ptr()), dt,
+                                                 ctypes.c_void_p(s.cuda_stream)))
+        self._guard(out, s)
+        return out
+
+    def split_moments(self, values):
+        """Views of `values` (pack_moments' layout) by tensor: a list of
+        (first, second) pairs, each rows x cols, in the order of the packed
+        tensors."""
+        pairs, at = [], 0
+        for d in self._descs[:self._n]:
+            if d.kind == KIND_ADAMW and d.state_bits == 8:
+                n = d.rows * d.cols
+                pairs.append(tuple(values[k, at:at + n].view(d.rows, d.cols) for k in (0, 1)))
+                at += n
+        return pairs
 
     def set_adam_step(self, steps_taken: int, stream=None):
         """Resume the AdamW step count (steps already taken)."""

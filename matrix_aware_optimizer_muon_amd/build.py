@@ -22,7 +22,7 @@ DEBUG_OBJ = os.path.join(CSRC, "_build_debug")
 DEBUG_FLAGS = ["-DMUON_DEBUG_BOUNDS=1"]
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
-SOURCES = ["muon_host.cpp", "elementwise.hip", "ns_gemm.hip", "precond.hip", "adamw.hip"]
+SOURCES = ["muon_host.cpp", "elementwise.hip", "ns_gemm.hip", "precond.hip", "adamw.hip", "adamw_packed.hip", "grad_norm.hip"]
 
 ARCH = "gfx950"
 HIP_FLAGS = [

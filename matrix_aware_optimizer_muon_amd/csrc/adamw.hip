@@ -50,7 +50,7 @@ __device__ __forceinline__ float adamw_elem(float w, float g, float& m, float& v
 // segment is issued before the first wait.
 template <bool WF32>
 __device__ __forceinline__ void adamw_segment(const AdamDev& d, const AdamTask& tk, const AdamParams& p, float lr,
-                                              float inv_bc1, float inv_sqrt_bc2, int64_t j0) {
+                                              float factor, float inv_bc1, float inv_sqrt_bc2, int64_t j0) {
   using W = typename std::conditional<WF32, float, uint16_t>::type;
   const int64_t r = tk.row;
   W* prow = static_cast<W*>(d.param) + r * d.ld_param;
@@ -85,6 +85,7 @@ __device__ __forceinline__ void adamw_segment(const AdamDev& d, const AdamTask& 
   bool bad = false;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    g[e] *= factor;     // 1 without clipping: exact
     bad |= !isfinite(g[e]);
     w[e] = adamw_elem(w[e], g[e], m[e], v[e], p, lr, inv_bc1, inv_sqrt_bc2);
   }
@@ -112,11 +113,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamDev* __restri
   const AdamTask tk = tasks[blockIdx.x];
   const AdamDev& d = tensors[tk.tensor];
   const float lr = p.lr * d.lr_mult;
+  const float factor = p.factor ? gld<float>(p.factor) : 1.f;
   const float inv_bc1 = p.state->inv_bc1, inv_sqrt_bc2 = p.state->inv_sqrt_bc2;
   const int64_t j0 = tk.c0 + int64_t(threadIdx.x) * 8;
   if (j0 >= d.len) return;
-  if (d.f32) adamw_segment<true>(d, tk, p, lr, inv_bc1, inv_sqrt_bc2, j0);
-  else adamw_segment<false>(d, tk, p, lr, inv_bc1, inv_sqrt_bc2, j0);
+  if (d.f32) adamw_segment<true>(d, tk, p, lr, factor, inv_bc1, inv_sqrt_bc2, j0);
+  else adamw_segment<false>(d, tk, p, lr, factor, inv_bc1, inv_sqrt_bc2, j0);
 }
 
 }  // namespace

@@ -78,6 +78,7 @@ __device__ __forceinline__ void momentum_tile(const UnitDev& u, const EwTask& t,
   const int rows = u.rows, cols = u.cols;
   const float mu = p.mu;
   const float one_m = 1.0f - mu;
+  const float factor = p.factor ? gld<float>(p.factor) : 1.0f;   // 1 without clipping: the products are exact
   float ss = 0.f;
   bool bad = false;
 
@@ -125,6 +126,7 @@ __device__ __forceinline__ void momentum_tile(const UnitDev& u, const EwTask& t,
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float mn, un;
+      g[q][e] *= factor;
       if (p.sgd_form) {
         mn = fmaf(mu, m[q][e], g[q][e]);
         un = p.nesterov ? fmaf(mu, mn, g[q][e]) : mn;

@@ -2,7 +2,9 @@
 // tile lists, workspace carve-up), descriptor upload and kernel sequencing.
 //
 // Plan of one step:
-//   adamw     (2 launches, only with kind-ADAMW tensors: count tick, update)
+//   grad norm (2 launches, only with a maximum set: sums, norm and factor)
+//   adamw     (only with kind-ADAMW tensors: count tick, update of the tensors
+//             with float32 moments, update of those with 8-bit ones)
 //             Muon README "Usage"
 // then per NS-precision group, all matrices of the group at once:
 //   momentum  (1 launch)      Muon README "Hyperparameter tuning"
@@ -17,6 +19,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -43,6 +46,17 @@ struct Range {
 muon_status_t fail(muon_status_t s, const std::string& msg) {
   g_last_error = msg;
   return s;
+}
+
+// Runs the body of an entry point; an exception of the host library (no
+// memory for a plan or a message) becomes a status.
+template <typename F>
+muon_status_t guarded(F&& body) {
+  try {
+    return body();
+  } catch (const std::exception&) {
+    return MUON_ERR_UNSUPPORTED;
+  }
 }
 
 constexpr size_t kAlign = 256;
@@ -127,11 +141,21 @@ struct Plan {
   std::vector<int> adam_tensors;     // kind-ADAMW tensors, in tensor order
   std::vector<AdamTask> adam_tasks;
   size_t off_adam_dev = 0, off_adam_tasks = 0, off_adam_state = 0;
+  std::vector<int> packed_tensors;   // kind-ADAMW tensors with 8-bit moments, in tensor order
+  std::vector<int64_t> packed_value0;  // elements of the packed tensors before each
+  std::vector<PackedTask> packed_tasks;
+  int64_t packed_elems = 0;
+  size_t off_packed_dev = 0, off_packed_tasks = 0;
+  std::vector<int64_t> norm_chunk0;  // per tensor: gradient-norm chunks of the tensors before it
+  int64_t norm_chunks = 0;
+  bool with_norm = false;            // the workspace holds the gradient norm's table and sums
+  size_t off_norm_dev = 0, off_norm_part = 0, off_norm_state = 0;
   size_t off_flags = 0, off_partials = 0, off_norms = 0;
   size_t off_mpart = 0;              // refresh scratch (moment partials, float64 S^-1 sum), all slots
   size_t meta_bytes = 0, total = 0;
   int total_k1_tiles = 0;
   int64_t zero_bytes = 0;  // bytes of NS buffers (zero-filled at init)
+  bool has_adam() const { return !adam_tasks.empty() || !packed_tasks.empty(); }
 };
 
 bool finite(float x) { return std::isfinite(x); }
@@ -144,6 +168,36 @@ float shape_scale(int64_t rows, int64_t cols, int mode) {
     case MUON_SCALE_SPECTRAL: return float(std::sqrt(double(rows) / double(cols)));
     default: return 1.f;
   }
+}
+
+bool packed(const muon_tensor_t& t) { return t.kind == MUON_KIND_ADAMW && t.state_bits == 8; }
+
+// The caller's buffers of one tensor.
+struct Buffer { const void* p; size_t bytes; const char* what; };
+std::vector<Buffer> buffers(const muon_tensor_t& t) {
+  const size_t es = t.dtype == MUON_F32 ? 4 : 2;
+  auto span = [&](int64_t ld, size_t esz) { return size_t((t.rows - 1) * ld + t.cols) * esz; };
+  const size_t moment = packed(t) ? size_t(packed_bytes(t.rows * t.cols)) : span(t.ld_momentum, 4);
+  std::vector<Buffer> out = {{t.param, span(t.ld_param, es), "param"},
+                             {t.grad, span(t.ld_grad, es), "grad"},
+                             {t.momentum, moment, "momentum"}};
+  if (t.update_out) out.push_back({t.update_out, span(t.cols, 4), "update_out"});
+  if (t.exp_avg_sq) out.push_back({t.exp_avg_sq, moment, "exp_avg_sq"});
+  return out;
+}
+
+// Whether [p, p + bytes) touches a buffer of a tensor; `who` gets its name.
+bool overlaps_tensors(const void* p, size_t bytes, const muon_tensor_t* ts, size_t n, std::string* who) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
+  for (size_t i = 0; i < n; ++i)
+    for (const Buffer& b : buffers(ts[i])) {
+      const uintptr_t blo = reinterpret_cast<uintptr_t>(b.p);
+      if (blo < hi && lo < blo + b.bytes) {
+        *who = "tensor " + std::to_string(i) + " " + b.what;
+        return true;
+      }
+    }
+  return false;
 }
 
 muon_status_t validate(const muon_tensor_t* ts, int32_t n, const muon_precond_t* pcs, int32_t npc,
@@ -187,10 +241,21 @@ muon_status_t validate(const muon_tensor_t* ts, int32_t n, const muon_precond_t*
     if (t.kind != MUON_KIND_MUON && t.kind != MUON_KIND_ADAMW)
       return fail(MUON_ERR_BAD_ARG, who + "kind must be MUON_KIND_MUON or MUON_KIND_ADAMW");
     const bool adam = t.kind == MUON_KIND_ADAMW;
+    if (t.state_bits != 0 && t.state_bits != 32 && t.state_bits != 8)
+      return fail(MUON_ERR_BAD_ARG, who + "state_bits must be 0, 32 or 8");
+    if (t.state_bits == 8 && !adam)
+      return fail(MUON_ERR_UNSUPPORTED, who + "8-bit moments are for AdamW tensors");
     if (adam) {
       if (!t.exp_avg_sq) return fail(MUON_ERR_NULL_ARG, who + "an AdamW tensor needs exp_avg_sq");
       if (t.split_rows != 0 || t.precond != -1 || t.update_out)
         return fail(MUON_ERR_BAD_ARG, who + "an AdamW tensor takes no split_rows, precond or update_out");
+      if (packed(t)) {
+        if (t.ld_momentum != t.cols)
+          return fail(MUON_ERR_BAD_SHAPE, who + "8-bit moments are contiguous: ld_momentum must equal cols");
+        if (t.rows * t.cols > kPackMaxElems) return fail(MUON_ERR_UNSUPPORTED, who + "too large for 8-bit moments");
+        if (reinterpret_cast<uintptr_t>(t.momentum) % 16 || reinterpret_cast<uintptr_t>(t.exp_avg_sq) % 16)
+          return fail(MUON_ERR_ALIGNMENT, who + "8-bit moments must be 16-byte aligned");
+      }
       if (reinterpret_cast<uintptr_t>(t.exp_avg_sq) % 4) return fail(MUON_ERR_ALIGNMENT, who + "exp_avg_sq misaligned");
     } else if (t.exp_avg_sq) {
       return fail(MUON_ERR_BAD_ARG, who + "exp_avg_sq is only for AdamW tensors");
@@ -213,16 +278,10 @@ muon_status_t validate(const muon_tensor_t* ts, int32_t n, const muon_precond_t*
     const int64_t TE = t.dtype == MUON_F32 ? kTileF32 : kTileEdgeM;   // units are padded to 128
     if (!adam && round_up(m, TE) * round_up(nn, TE) > (int64_t(1) << 31))
       return fail(MUON_ERR_UNSUPPORTED, who + "matrix too large for one orthogonalisation unit");
-    auto add = [&](const void* p, int64_t ld, size_t esz, const char* what) {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      const uintptr_t hi = lo + (size_t((t.rows - 1) * ld + t.cols)) * esz;
-      ranges.push_back({lo, hi, i, what});
-    };
-    add(t.param, t.ld_param, es, "param");
-    add(t.grad, t.ld_grad, es, "grad");
-    add(t.momentum, t.ld_momentum, 4, "momentum");
-    if (t.update_out) add(t.update_out, t.cols, 4, "update_out");
-    if (t.exp_avg_sq) add(t.exp_avg_sq, t.ld_momentum, 4, "exp_avg_sq");
+    for (const Buffer& b : buffers(t)) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(b.p);
+      ranges.push_back({lo, lo + b.bytes, i, b.what});
+    }
   }
   std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
   for (size_t k = 1; k < ranges.size(); ++k)
@@ -384,7 +443,7 @@ bool tiles_cover_exactly(const std::vector<UnitPlan>& units, const Group& g) {
 }
 
 muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_t* pcs, int32_t npc,
-                         const muon_hparams_t* hp, Plan& plan, bool single_lane = false) {
+                         const muon_hparams_t* hp, Plan& plan, bool single_lane = false, bool with_norm = true) {
   muon_status_t st = validate(ts, n, pcs, npc, hp);
   if (st != MUON_OK) return st;
   plan = Plan();
@@ -417,12 +476,25 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   for (int32_t i = 0; i < n; ++i) {
     const muon_tensor_t& t = ts[i];
     if (t.kind != MUON_KIND_ADAMW) continue;
+    if (packed(t)) {
+      const int pi = int(plan.packed_tensors.size());
+      plan.packed_tensors.push_back(i);
+      plan.packed_value0.push_back(plan.packed_elems);
+      for (int64_t c0 = 0; c0 < t.rows * t.cols; c0 += kPackChunk) plan.packed_tasks.push_back({pi, 0, c0});
+      plan.packed_elems += t.rows * t.cols;
+      continue;
+    }
     const int ai = int(plan.adam_tensors.size());
     plan.adam_tensors.push_back(i);
     const bool flat = t.ld_param == t.cols && t.ld_grad == t.cols && t.ld_momentum == t.cols;
     const int64_t nrows = flat ? 1 : t.rows, len = flat ? t.rows * t.cols : t.cols;
     for (int64_t r = 0; r < nrows; ++r)
       for (int64_t c0 = 0; c0 < len; c0 += kAdamChunk) plan.adam_tasks.push_back({ai, int32_t(r), c0});
+  }
+  plan.with_norm = with_norm;
+  for (int32_t i = 0; i < n; ++i) {
+    plan.norm_chunk0.push_back(plan.norm_chunks);
+    plan.norm_chunks += (ts[i].rows * ts[i].cols + kNormChunk - 1) / kNormChunk;
   }
   // units
   for (int32_t i = 0; i < n; ++i) {
@@ -554,6 +626,13 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   plan.off_adam_dev = off; off = align_up(off + sizeof(AdamDev) * plan.adam_tensors.size());
   plan.off_adam_tasks = off; off = align_up(off + sizeof(AdamTask) * plan.adam_tasks.size());
   plan.off_adam_state = off; off = align_up(off + sizeof(AdamState));
+  plan.off_packed_dev = off; off = align_up(off + sizeof(PackedDev) * plan.packed_tensors.size());
+  plan.off_packed_tasks = off; off = align_up(off + sizeof(PackedTask) * plan.packed_tasks.size());
+  if (plan.with_norm) {
+    plan.off_norm_dev = off; off = align_up(off + sizeof(NormDev) * size_t(n));
+    plan.off_norm_part = off; off = align_up(off + sizeof(double) * size_t(std::min<int64_t>(plan.norm_chunks, kNormBlocks)));
+    plan.off_norm_state = off; off = align_up(off + sizeof(NormState));
+  }
   plan.meta_bytes = off;
   for (UnitPlan& u : plan.units) {
     const size_t es = u.f32 ? 4 : 2;
@@ -691,6 +770,48 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
   }
   if (!plan.adam_tasks.empty())
     std::memcpy(meta.data() + plan.off_adam_tasks, plan.adam_tasks.data(), plan.adam_tasks.size() * sizeof(AdamTask));
+  auto al16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  for (size_t pi = 0; pi < plan.packed_tensors.size(); ++pi) {
+    const muon_tensor_t& t = ts[plan.packed_tensors[pi]];
+    const int64_t es = t.dtype == MUON_F32 ? 4 : 2;
+    PackedDev d;
+    std::memset(&d, 0, sizeof(d));
+    d.param = t.param;
+    d.grad = t.grad;
+    d.m = reinterpret_cast<uint8_t*>(t.momentum);
+    d.v = reinterpret_cast<uint8_t*>(t.exp_avg_sq);
+    d.ld_param = t.ld_param;
+    d.ld_grad = t.ld_grad;
+    d.n = t.rows * t.cols;
+    d.cols = t.cols;
+    d.blocks = packed_blocks(d.n);
+    d.value0 = plan.packed_value0[pi];
+    d.f32 = t.dtype == MUON_F32;
+    d.flat = t.rows == 1 || (t.ld_param == t.cols && t.ld_grad == t.cols);
+    d.vec = al16(t.param) && al16(t.grad) &&
+            (d.flat || (t.cols % 16 == 0 && (t.ld_param * es) % 16 == 0 && (t.ld_grad * es) % 16 == 0));
+    d.tensor = uint32_t(plan.packed_tensors[pi]);
+    d.lr_mult = t.lr_mult;
+    std::memcpy(meta.data() + plan.off_packed_dev + pi * sizeof(PackedDev), &d, sizeof(d));
+  }
+  if (!plan.packed_tasks.empty())
+    std::memcpy(meta.data() + plan.off_packed_tasks, plan.packed_tasks.data(),
+                plan.packed_tasks.size() * sizeof(PackedTask));
+  for (size_t i = 0; plan.with_norm && i < plan.norm_chunk0.size(); ++i) {
+    const muon_tensor_t& t = ts[i];
+    const int64_t es = t.dtype == MUON_F32 ? 4 : 2;
+    NormDev d;
+    std::memset(&d, 0, sizeof(d));
+    d.grad = t.grad;
+    d.ld = t.ld_grad;
+    d.n = t.rows * t.cols;
+    d.cols = t.cols;
+    d.chunk0 = plan.norm_chunk0[i];
+    d.f32 = t.dtype == MUON_F32;
+    d.flat = t.rows == 1 || t.ld_grad == t.cols;
+    d.vec = al16(t.grad) && (d.flat || (t.cols % 8 == 0 && (t.ld_grad * es) % 16 == 0));
+    std::memcpy(meta.data() + plan.off_norm_dev + i * sizeof(NormDev), &d, sizeof(d));
+  }
   return meta;
 }
 
@@ -710,6 +831,9 @@ struct muon_handle_s {
   hipEvent_t ev_fork = nullptr;
   std::vector<hipEvent_t> events;
   std::vector<std::string> phase_names;
+  float max_norm = 0.f;          // > 0: every step clips by the global gradient norm
+  float* norm_out = nullptr;     // where the caller wants the norm and the factor, or NULL
+  uint64_t rounding_seed = 0;
   int static_device = -1;        // muon_init_static: the GPU whose scratch array holds the workspace
   uint64_t static_generation = 0;  // ... and which of its static inits this handle is
 };
@@ -728,6 +852,18 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
   };
   Range step_range("muon.step");
   if (!mark()) return fail(MUON_ERR_HIP, "hipEventRecord failed");
+  // before the fork: every gradient's reader multiplies by the factor
+  const float* factor = nullptr;
+  if (h->max_norm > 0.f) {
+    Range r("muon.grad_norm");
+    NormState* ns = reinterpret_cast<NormState*>(h->ws + plan.off_norm_state);
+    hipError_t e = launch_grad_norm(reinterpret_cast<const NormDev*>(h->ws + plan.off_norm_dev),
+                                    int(h->tensors.size()), plan.norm_chunks,
+                                    reinterpret_cast<double*>(h->ws + plan.off_norm_part), ns, h->max_norm,
+                                    h->norm_out, s);
+    if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("grad norm launch: ") + hipGetErrorString(e));
+    factor = &ns->factor;
+  }
   if (!plan.apply.empty()) {
     Range r("muon.precond_apply");
     hipError_t e = launch_precond_apply(reinterpret_cast<const PrecondDev*>(h->ws + plan.off_pdev),
@@ -753,18 +889,23 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     AdamState* st = reinterpret_cast<AdamState*>(h->ws + plan.off_adam_state);
     hipError_t e = launch_adam_tick(st, hp.adam_beta1, hp.adam_beta2, as);
     AdamParams ap{hp.adam_lr, hp.adam_beta1, hp.adam_beta2, hp.adam_eps, hp.adam_weight_decay, st,
-                  reinterpret_cast<uint32_t*>(h->ws + plan.off_flags)};
+                  reinterpret_cast<uint32_t*>(h->ws + plan.off_flags), factor};
     if (e == hipSuccess)
       e = launch_adamw(reinterpret_cast<const AdamDev*>(h->ws + plan.off_adam_dev),
                        reinterpret_cast<const AdamTask*>(h->ws + plan.off_adam_tasks), int(plan.adam_tasks.size()),
                        ap, as);
+    if (e == hipSuccess && !plan.packed_tasks.empty())
+      e = launch_adamw_packed(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
+                              reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
+                              int(plan.packed_tasks.size()),
+                              PackedParams{ap, uint32_t(h->rounding_seed), uint32_t(h->rounding_seed >> 32)}, as);
     if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("adamw launch: ") + hipGetErrorString(e));
     return MUON_OK;
   };
   // AdamW is HBM-bound like the momentum phase: on its own stream it starts
   // once the first lane's momentum launch is done, beside the MFMA phases
-  const bool adam_aside = fork && h->aux_stream != nullptr && !plan.adam_tasks.empty();
-  if (!plan.adam_tasks.empty() && !adam_aside) {
+  const bool adam_aside = fork && h->aux_stream != nullptr && plan.has_adam();
+  if (plan.has_adam() && !adam_aside) {
     const muon_status_t st = launch_adam(s);
     if (st != MUON_OK) return st;
   }
@@ -774,7 +915,7 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     const hipStream_t gs = fork && g.lane > 0 ? h->lane_streams[g.lane - 1] : s;
     const UnitDev* units = reinterpret_cast<const UnitDev*>(h->ws + g.off_units);
     K1Params k1{hp.momentum, hp.nesterov, hp.momentum_form == MUON_MOM_SGD,
-                reinterpret_cast<uint32_t*>(h->ws + plan.off_flags)};
+                reinterpret_cast<uint32_t*>(h->ws + plan.off_flags), factor};
     hipError_t e;
     {
       Range r("muon.momentum");
@@ -887,16 +1028,20 @@ std::string plan_json(const Plan& plan, const muon_hparams_t& hp) {
     s += buf;
   }
   std::snprintf(buf, sizeof(buf), "],\"apply_tiles\":%zu,\"adamw_tensors\":%zu,\"adamw_tasks\":%zu,"
-                "\"launch_order\":[", plan.apply.size(), plan.adam_tensors.size(), plan.adam_tasks.size());
+                "\"packed_tensors\":%zu,\"packed_tasks\":%zu,\"launch_order\":[", plan.apply.size(),
+                plan.adam_tensors.size(), plan.adam_tasks.size(), plan.packed_tensors.size(),
+                plan.packed_tasks.size());
   s += buf;
   first = true;
   if (!plan.apply.empty()) {
     s += "\"precond_apply\"";
     first = false;
   }
-  if (!plan.adam_tasks.empty()) {
+  if (plan.has_adam()) {
     if (!first) s += ",";
-    s += "\"adam_tick\",\"adamw\"";
+    s += "\"adam_tick\"";
+    if (!plan.adam_tasks.empty()) s += ",\"adamw\"";
+    if (!plan.packed_tasks.empty()) s += ",\"adamw_packed\"";
     first = false;
   }
   for (const Group& g : plan.groups) {
@@ -1014,21 +1159,9 @@ muon_status_t static_scratch(int* dev_out, void** ptr_out) {
 // caller's stream.
 muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* tensors, int32_t n_tensors,
                           const muon_hparams_t* hp, void* workspace, void* stream, bool with_streams) {
-  const uintptr_t wlo = reinterpret_cast<uintptr_t>(workspace), whi = wlo + plan.total;
-  for (int32_t i = 0; i < n_tensors; ++i) {
-    const muon_tensor_t& t = tensors[i];
-    const size_t es = t.dtype == MUON_F32 ? 4 : 2;
-    const void* ps[5] = {t.param, t.grad, t.momentum, t.update_out, t.exp_avg_sq};
-    const int64_t lds[5] = {t.ld_param, t.ld_grad, t.ld_momentum, t.cols, t.ld_momentum};
-    const size_t ess[5] = {es, es, 4, 4, 4};
-    for (int k = 0; k < 5; ++k) {
-      if (!ps[k]) continue;
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(ps[k]);
-      const uintptr_t hi = lo + size_t((t.rows - 1) * lds[k] + t.cols) * ess[k];
-      if (lo < whi && wlo < hi)
-        return fail(MUON_ERR_ALIASING, "tensor " + std::to_string(i) + " overlaps the workspace");
-    }
-  }
+  std::string who;
+  if (overlaps_tensors(workspace, plan.total, tensors, size_t(n_tensors), &who))
+    return fail(MUON_ERR_ALIASING, who + " overlaps the workspace");
   muon_handle_s* h = new (std::nothrow) muon_handle_s();
   if (!h) return fail(MUON_ERR_UNSUPPORTED, "host allocation failed");
   h->plan = std::move(plan);
@@ -1049,7 +1182,7 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   h->last_stream = s;
   int max_lane = 0;
   for (const Group& g : h->plan.groups) max_lane = std::max(max_lane, g.lane);
-  const bool aux = with_streams && !h->plan.adam_tasks.empty() && !h->plan.units.empty();
+  const bool aux = with_streams && h->plan.has_adam() && !h->plan.units.empty();
   if (with_streams && (max_lane > 0 || aux)) {
     e = hipEventCreateWithFlags(&h->ev_fork, hipEventDisableTiming);
     if (aux && e == hipSuccess) e = hipStreamCreateWithFlags(&h->aux_stream, hipStreamNonBlocking);
@@ -1075,7 +1208,7 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
     }
   }
   if (!h->plan.apply.empty()) h->phase_names.push_back("precond_apply");
-  if (!h->plan.adam_tasks.empty()) h->phase_names.push_back("adamw");
+  if (h->plan.has_adam()) h->phase_names.push_back("adamw");
   for (const Group& g : h->plan.groups) {
     if (g.units.empty()) continue;
     const std::string dt = std::string(g.f32 ? "/f32" : "/bf16") + (g.lane ? "@" + std::to_string(g.lane + 1) : "");
@@ -1132,6 +1265,8 @@ muon_status_t muon_init_static(muon_handle_t* out, const muon_tensor_t* tensors,
   *out = nullptr;
   Plan plan;
   muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true);
+  if (st == MUON_OK && plan.total > kStaticScratchBytes)   // the gradient norm's table may be what does not fit
+    st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true, /*with_norm=*/false);
   if (st != MUON_OK) return st;
   if (plan.total > kStaticScratchBytes)
     return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
@@ -1175,6 +1310,30 @@ muon_status_t check_slot_block(muon_handle_t h, int32_t slot, int32_t block) {
   if (slot < 0 || size_t(slot) >= h->plan.slots.size()) return fail(MUON_ERR_BAD_ARG, "no such preconditioner slot");
   if (block < 0 || block >= h->plan.slots[size_t(slot)].nblocks) return fail(MUON_ERR_BAD_ARG, "no such block in the slot");
   return MUON_OK;
+}
+
+// A buffer that a call reads or writes beside the registered ones.
+muon_status_t check_apart(muon_handle_t h, const void* p, size_t bytes, const char* what) {
+  std::string who;
+  if (overlaps_tensors(p, bytes, h->tensors.data(), h->tensors.size(), &who))
+    return fail(MUON_ERR_ALIASING, std::string(what) + " overlaps " + who);
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), wlo = reinterpret_cast<uintptr_t>(h->ws);
+  if (lo < wlo + h->plan.total && wlo < lo + bytes)
+    return fail(MUON_ERR_ALIASING, std::string(what) + " overlaps the workspace");
+  return MUON_OK;
+}
+
+// The values of every packed moment, as muon_pack_moments and
+// muon_unpack_moments take them.
+muon_status_t check_values(muon_handle_t h, const void* values, int32_t dtype) {
+  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+  if (dtype != MUON_F32 && dtype != MUON_BF16) return fail(MUON_ERR_BAD_DTYPE, "values must be f32 or bf16");
+  if (h->plan.packed_elems == 0) return MUON_OK;
+  if (!values) return fail(MUON_ERR_NULL_ARG, "values is NULL");
+  const size_t es = dtype == MUON_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(values) % es) return fail(MUON_ERR_ALIGNMENT, "values misaligned");
+  return check_apart(h, values, 2 * size_t(h->plan.packed_elems) * es, "values");
 }
 
 muon_status_t check_acts(const SlotPlan& sp, const void* acts, int64_t n_rows, int64_t ld, int32_t dtype) {
@@ -1296,6 +1455,71 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
   if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step read: ") + hipGetErrorString(e));
   *steps_taken = int64_t(st.t);
   return MUON_OK;
+}
+
+size_t muon_packed_moment_bytes(int64_t n) { return n > 0 && n <= kPackMaxElems ? size_t(packed_bytes(n)) : 0; }
+
+muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed) {
+  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+  h->rounding_seed = seed;
+  return MUON_OK;
+}
+
+muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* norm_out) {
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (!(max_norm >= 0.f)) return fail(MUON_ERR_BAD_ARG, "max_norm must be >= 0");
+    if (max_norm == 0.f) norm_out = nullptr;
+    if (max_norm > 0.f && !h->plan.with_norm)
+      return fail(MUON_ERR_WORKSPACE_TOO_SMALL, "the static scratch has no room for the gradient norm's sums "
+                                                "(use muon_init with a caller workspace)");
+    if (norm_out) {
+      if (reinterpret_cast<uintptr_t>(norm_out) % 4) return fail(MUON_ERR_ALIGNMENT, "norm_out misaligned");
+      const muon_status_t st = check_apart(h, norm_out, 2 * sizeof(float), "norm_out");
+      if (st != MUON_OK) return st;
+    }
+    const bool was = h->max_norm > 0.f, is = max_norm > 0.f;
+    if (is && !was) h->phase_names.insert(h->phase_names.begin(), "grad_norm");
+    if (was && !is) h->phase_names.erase(h->phase_names.begin());
+    h->max_norm = max_norm;
+    h->norm_out = norm_out;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_pack_moments(muon_handle_t h, const void* values, int32_t dtype, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_values(h, values, dtype);
+    if (st != MUON_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Plan& plan = h->plan;
+    if (plan.packed_tasks.empty()) return MUON_OK;
+    Range r("muon.pack_moments");
+    hipError_t e = launch_pack_moments(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
+                                       reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
+                                       int(plan.packed_tasks.size()), values, plan.packed_elems, dtype == MUON_F32,
+                                       reinterpret_cast<uint32_t*>(h->ws + plan.off_flags), s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("pack moments launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_values(h, values, dtype);
+    if (st != MUON_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Plan& plan = h->plan;
+    if (plan.packed_tasks.empty()) return MUON_OK;
+    Range r("muon.unpack_moments");
+    hipError_t e = launch_unpack_moments(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
+                                         reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
+                                         int(plan.packed_tasks.size()), values, plan.packed_elems, dtype == MUON_F32, s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("unpack moments launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_get_flags(muon_handle_t h, void* stream, int32_t reset, uint32_t* flags) {

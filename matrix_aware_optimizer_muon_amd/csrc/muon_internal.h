@@ -75,6 +75,7 @@ struct K1Params {
   int32_t nesterov;
   int32_t sgd_form;
   uint32_t* flags;
+  const float* factor; // clipping factor of every gradient, on the device (NULL: 1)
 };
 
 struct GemmParams {
@@ -182,7 +183,50 @@ struct AdamParams {
   float lr, beta1, beta2, eps, weight_decay;
   const AdamState* state;
   uint32_t* flags;
+  const float* factor;                 // clipping factor of every gradient, on the device (NULL: 1)
 };
+
+// AdamW tensors whose moments are packed: one byte an element, in blocks of
+// kPackBlock consecutive elements of the row-major tensor, and one 16-bit
+// scale a block behind the bytes of all blocks (adamw_packed.hip has the
+// formats).
+constexpr int kPackBlock = 256;
+constexpr int kPackChunk = 4096;       // elements per thread block (256 threads x 16)
+constexpr int64_t kPackMaxElems = int64_t(1) << 35;   // element / 16 fits the 32-bit counter of the random words
+inline int64_t packed_blocks(int64_t n) { return (n + kPackBlock - 1) / kPackBlock; }
+inline int64_t packed_bytes(int64_t n) { return packed_blocks(n) * (kPackBlock + 2); }
+struct PackedDev {
+  void* param; const void* grad;
+  uint8_t* m; uint8_t* v;              // codes; the scales are at + kPackBlock * blocks
+  int64_t ld_param, ld_grad;           // elements between rows
+  int64_t n, cols;                     // elements in all, and per row
+  int64_t blocks;
+  int64_t value0;                      // elements of the packed tensors before this one
+  int32_t f32;                         // param/grad float32 (else bf16)
+  int32_t flat;                        // element i of param and grad lies at i
+  int32_t vec;                         // groups of 16 elements are contiguous and 16-byte aligned
+  uint32_t tensor;                     // its place in the registered list (random words)
+  float lr_mult;
+  int32_t pad;
+};
+struct PackedTask { int32_t tensor, pad; int64_t c0; };
+struct PackedParams {
+  AdamParams adam;
+  uint32_t seed_lo, seed_hi;
+};
+
+// Global gradient norm: every registered gradient as a run of n elements cut
+// in chunks of kNormChunk, the chunks of all tensors numbered through; each
+// block sums a contiguous range of them.
+constexpr int kNormChunk = 8192;       // 256 threads x 32 elements
+constexpr int kNormBlocks = 2048;      // most blocks (and partial sums)
+struct NormDev {
+  const void* grad;
+  int64_t ld, n, cols;                 // cols: row length, of use only where flat is 0
+  int64_t chunk0;                      // chunks of the tensors before this one
+  int32_t f32, flat, vec, pad;         // vec: groups of 8 elements are contiguous and 16-byte aligned
+};
+struct NormState { float norm, factor; };   // of the latest step, in the workspace
 
 hipError_t launch_momentum(bool f32, const UnitDev* units, const EwTask* tasks, int n_tasks,
                            const K1Params& p, hipStream_t s);
@@ -203,5 +247,19 @@ hipError_t launch_adam_tick(AdamState* st, float beta1, float beta2, hipStream_t
 hipError_t launch_adam_set(AdamState* st, uint32_t t, hipStream_t s);
 hipError_t launch_adamw(const AdamDev* tensors, const AdamTask* tasks, int n_tasks, const AdamParams& p,
                         hipStream_t s);
+
+// Weak: the planner also links, and plans, without the kernels below.
+#define MUON_WEAK __attribute__((weak))
+MUON_WEAK hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
+                                         const PackedParams& p, hipStream_t s);
+// values: n_values first moments, then n_values second ones, float32 or bf16
+MUON_WEAK hipError_t launch_pack_moments(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
+                                         const void* values, int64_t n_values, bool f32, uint32_t* flags,
+                                         hipStream_t s);
+MUON_WEAK hipError_t launch_unpack_moments(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
+                                           void* values, int64_t n_values, bool f32, hipStream_t s);
+// norm_out: NULL, or two floats that get the state as well
+MUON_WEAK hipError_t launch_grad_norm(const NormDev* tensors, int n_tensors, int64_t n_chunks, double* partials,
+                                      NormState* state, float max_norm, float* norm_out, hipStream_t s);
 
 }  // namespace muon

@@ -1,0 +1,161 @@
+"""What pins the oracle of the packed moments (CPU only): the number formats
+against torch's float8 type and float32's own spacing, the bounds the header
+states, the mean of the random rounding, and planted mistakes."""
+
+import numpy as np
+import pytest
+
+from oracle import packed_moments as pm
+
+torch = pytest.importorskip("torch")
+
+
+def _rng(*key):
+    return np.random.Generator(np.random.PCG64(np.random.SeedSequence([9100, *key])))
+
+
+def _wide(rng, n, decades=4.0):
+    return (rng.normal(0, 1, n) * 10.0 ** rng.uniform(-decades, 0, n)).astype(np.float32)
+
+
+def test_e4m3_is_the_float8_type():
+    codes = torch.arange(256, dtype=torch.uint8)
+    ref = codes.view(torch.float8_e4m3fn).float().numpy()
+    got = pm.E4M3[codes.numpy() & 127] * np.where(codes.numpy() & 128, -1, 1)
+    assert np.array_equal(ref, got, equal_nan=True)
+
+
+def test_nearest_is_the_float8_conversion():
+    rng = _rng(1)
+    x = rng.uniform(-448, 448, 4096).astype(np.float32) * (2.0 ** -rng.integers(0, 12, 4096)).astype(np.float32)
+    x[::256] = 448.0        # fixes every block's scale at 1
+    first, _ = pm.encode(x, np.zeros_like(x))
+    ref = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(first[:4096], ref)
+    assert np.array_equal(first[4096:].view("<u2"), np.full(16, 127))
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "random"])
+@pytest.mark.parametrize("n", [1, 255, 256, 257, 5000])
+def test_stated_bounds(n, rounding):
+    rng = _rng(2, n)
+    m, v = _wide(rng, n), _wide(rng, n) ** 2
+    word = None if rounding == "nearest" else pm.words(5, 7, 1, n)
+    first, second = pm.encode(m, v, word)
+    assert first.size == second.size == pm.moment_bytes(n)
+    dm, dv = pm.decode(first, second, n)
+    blocks = np.arange(n) // pm.BLOCK
+    mx = np.array([np.abs(m[blocks == b]).max() for b in range(blocks[-1] + 1)])[blocks]
+    vx = np.array([v[blocks == b].max() for b in range(blocks[-1] + 1)])[blocks]
+    # nearest: half a step; e4m3: 3 mantissa bits, and 2^-9 of a unit of at most max / 224 below 2^-6
+    k = 1.0 if rounding == "nearest" else 2.0
+    assert (np.abs(dm - m) <= k * np.maximum(np.abs(m) / 16, mx / 224 * 2.0 ** -10)).all()
+    # code 1 stands 254 places, 31.75 binades, below the scale's top, which is at most 1.125 of the largest
+    held = v > vx * 2.0 ** -31
+    assert (np.abs(dv - v) <= k * v / 16)[held].all() and (dv <= vx * 2.0 ** -31)[~held].all()
+    assert ((dv > 0) == (v > 0)).all()
+
+
+def test_zeros_tiny_and_overflowing_blocks():
+    z = np.zeros(300, np.float32)
+    for word in (None, pm.words(0, 1, 0, 300)):
+        dm, dv = pm.decode(*pm.encode(z, z, word), 300)
+        assert not dm.any() and not dv.any()
+    dm, dv = pm.decode(np.zeros(pm.moment_bytes(300), np.uint8), np.zeros(pm.moment_bytes(300), np.uint8), 300)
+    assert not dm.any() and not dv.any()
+    # a second moment far below its block's largest is raised, never lost
+    v = np.full(256, 1e-30, np.float32)
+    v[0] = 1.0
+    _, dv = pm.decode(*pm.encode(z[:256], v), 256)
+    assert dv[0] == 1.0 and (dv[1:] > 0).all() and (dv[1:] <= 2.0 ** -31).all()
+    # not finite: NaN there, the rest of the block as if it were zero
+    m = _wide(_rng(3), 256)
+    ref, _ = pm.decode(*pm.encode(np.where(np.arange(256) == 7, 0, m).astype(np.float32), v), 256)
+    for bad in (np.nan, np.inf, -np.inf):
+        m[7] = bad
+        dm, _ = pm.decode(*pm.encode(m, v), 256)
+        assert np.isnan(dm[7]) and np.array_equal(np.delete(dm, 7), np.delete(ref, 7))
+    v[3] = np.inf
+    _, dv = pm.decode(*pm.encode(z[:256], v), 256)
+    assert dv[3] == 1.875 * 2.0 ** 127
+
+
+def test_random_rounding_has_the_value_as_its_mean():
+    # 2^14 roundings of each of 256 values.  The mean of N roundings is off by
+    # at most 6 standard deviations (a step's half / sqrt(N) each) but for a
+    # chance of 2e-9 a value; the 20-bit share adds at most 2^-20 of a step.
+    rng, n = _rng(4), 256
+    m, v = _wide(rng, n, 3.0), (10.0 ** rng.uniform(-8, 0, n)).astype(np.float32)
+    N = 1 << 14
+    sm, sv = np.zeros(n), np.zeros(n)
+    for t in range(N // 64):
+        for k in range(64):
+            dm, dv = pm.decode(*pm.encode(m, v, pm.words(11, t, k, n)), n)
+            sm += dm
+            sv += dv
+    step_m = np.maximum(np.abs(m) / 8, np.abs(m).max() / 224 * 2.0 ** -9)
+    step_v = v / 8
+    tol = 6 * 0.5 / np.sqrt(N) + 2.0 ** -20
+    assert (np.abs(sm / N - m) <= tol * step_m).all()
+    assert (np.abs(sv / N - v) <= tol * step_v).all()
+
+
+def test_words_are_even_and_differ_by_seed_step_tensor_and_element():
+    n = 1 << 16
+    base = pm.words(1, 2, 3, n)
+    for other in (pm.words(2, 2, 3, n), pm.words(1 << 32 | 1, 2, 3, n), pm.words(1, 3, 3, n), pm.words(1, 2, 4, n)):
+        assert (base == other).mean() < 1e-3
+        # the shares that round the same element in two steps do not go together: 1/sqrt(12) spread each,
+        # the mean product of n of them is within 6 / (12 sqrt(n))
+        for sh in (12, 0):
+            a = ((base >> np.uint32(sh)) & 0xFFFFF) / 2.0 ** 20 - 0.5
+            b = ((other >> np.uint32(sh)) & 0xFFFFF) / 2.0 ** 20 - 0.5
+            assert abs((a * b).mean()) < 6 / 12 / np.sqrt(n / 16)   # 16 elements share a hash
+    for sh in (12, 0):
+        share = ((base >> np.uint32(sh)) & 0xFFFFF) / 2.0 ** 20
+        hist = np.histogram(share, 64, (0, 1))[0]
+        assert np.abs(hist - n / 64).max() < 6 * np.sqrt(n / 64)
+
+
+def test_a_vanished_gradient_decays_only_with_random_rounding():
+    # 8 values a binade: a decay by 5 % is under half a step, so rounding to
+    # nearest holds v where it is; at random it follows beta2^t in the mean
+    n, b2, steps = 4096, np.float32(0.95), 40
+    v0 = np.full(n, np.float32(1.125))
+    z = np.zeros(n, np.float32)
+    stuck, rand = v0.astype(np.float64), v0.astype(np.float64)
+    for t in range(steps):
+        _, stuck = pm.decode(*pm.encode(z, b2 * stuck.astype(np.float32)), n)
+        _, rand = pm.decode(*pm.encode(z, b2 * rand.astype(np.float32), pm.words(0, t, 0, n)), n)
+    assert (stuck == 1.125).all()
+    # spread of one element after many steps: 0.041 / sqrt(1 - b2^2) of it; 6 of those over sqrt(n), and
+    # the 16 elements of a hash counted as one
+    assert abs(rand.mean() / (1.125 * 0.95 ** steps) - 1) < 6 * 0.041 / np.sqrt(1 - 0.95 ** 2) / np.sqrt(n / 16)
+
+
+def test_planted_mistakes_show():
+    n = 512
+    rng = _rng(6)
+    m, v = _wide(rng, n), _wide(rng, n) ** 2
+    w = pm.words(3, 4, 5, n)
+    good = pm.encode(m, v, w)
+    dm, dv = pm.decode(*good, n)
+    swapped = pm.encode(m, v, (w >> np.uint32(12)) | (w << np.uint32(20)))        # the two shares exchanged
+    assert not np.array_equal(good[0], swapped[0]) and not np.array_equal(good[1], swapped[1])
+    late = pm.encode(m, v, pm.words(3, 5, 5, n))                                  # the step count off by one
+    assert not np.array_equal(good[0], late[0])
+    scaled = good[0].copy()
+    scaled[n:].view("<u2")[0] += 1                                                # a scale off by one
+    assert np.abs(pm.decode(scaled, good[1], n)[0][:256] - m[:256]).max() > np.abs(m[:256]).max() / 8
+    lost = good[1].copy()
+    lost[:n][lost[:n] == lost[:n].min()] = 0                                      # a second moment rounded to zero
+    assert ((pm.decode(good[0], lost, n)[1] > 0) != (v > 0)).any()
+
+
+def test_clip_factor():
+    g = [np.array([3.0, 0.0]), np.array([[4.0]])]
+    assert pm.clip(g, 10.0) == (5.0, 1.0)
+    assert pm.clip(g, 5.0) == (5.0, 1.0)
+    assert pm.clip(g, 1.0) == (5.0, 0.2)
+    assert np.isnan(pm.clip([np.array([np.nan])], 1.0)[1])
+    assert pm.clip([np.array([np.inf])], 1.0) == (np.inf, 0.0)
