@@ -357,6 +357,8 @@ class MuonStep:
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._keep = list(keepalive)
+        self._packed_elements = sum(d.rows * d.cols for d in self._descs[:self._n]
+                                    if d.kind == KIND_ADAMW and d.state_bits == 8)
         self.grad_norm = None
         h = ctypes.c_void_p()
         if static_scratch:
@@ -472,19 +474,25 @@ class MuonStep:
 
     def packed_elements(self) -> int:
         """Elements of all tensors with packed moments."""
-        return sum(d.rows * d.cols for d in self._descs[:self._n] if d.kind == KIND_ADAMW and d.state_bits == 8)
+        return self._packed_elements
+
+    def _check_values(self, values, name):
+        """The ABI's dtype of a values tensor of all packed moments."""
+        torch = _torch()
+        n = self._packed_elements
+        if values.shape != (2, n) or not values.is_contiguous() or values.device != self.device:
+            raise ValueError(f"{name} must be a contiguous tensor of shape (2, {n}) on {self.device}")
+        if values.dtype == torch.float32:
+            return MUON_F32
+        if values.dtype == torch.bfloat16:
+            return MUON_BF16
+        raise ValueError(f"unsupported dtype {values.dtype}")
 
     def pack_moments(self, values, stream=None):
         """Set every packed moment from `values`, a contiguous float32 or
         bfloat16 tensor [2, packed_elements()]: the first moments of all packed
         tensors one after another, then the second ones (round to nearest)."""
-        torch = _torch()
-        n = self.packed_elements()
-        if tuple(values.shape) != (2, n) or not values.is_contiguous() or values.device != self.device:
-            raise ValueError(f"values must be a contiguous tensor of shape (2, {n}) on {self.device}")
-        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(values.dtype)
-        if dt is None:
-            raise ValueError(f"unsupported dtype {values.dtype}")
+        dt = self._check_values(values, "values")
         s = self._torch_stream(stream)
         with self._here():
             self._check(self._lib.muon_pack_moments(self._h, ctypes.c_void_p(values.data_ptr()), dt,
@@ -497,20 +505,18 @@ class MuonStep:
         float32), laid out as pack_moments takes it; into `out` if given.
         split_moments cuts it into the tensors' own."""
         torch = _torch()
-        n = self.packed_elements()
-        if out is None:
-            out = torch.empty(2, n, dtype=dtype or torch.float32, device=self.device)
-        elif tuple(out.shape) != (2, n) or not out.is_contiguous() or out.device != self.device \
-                or (dtype is not None and dtype != out.dtype):
-            raise ValueError(f"out must be a contiguous tensor of shape (2, {n}) on {self.device}, of dtype if given")
-        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(out.dtype)
-        if dt is None:
-            raise ValueError(f"unsupported dtype {out.dtype}")
+        fresh = out is None
+        if fresh:
+            out = torch.empty((2, self._packed_elements), dtype=dtype or torch.float32, device=self.device)
+        elif dtype is not None and dtype != out.dtype:
+            raise ValueError("out is not of the dtype asked for")
+        dt = self._check_values(out, "out")
         s = self._torch_stream(stream)
         with self._here():
             self._check(self._lib.muon_unpack_moments(self._h, ctypes.c_void_p(out.data_ptr()), dt,
                                                  ctypes.c_void_p(s.cuda_stream)))
-        self._guard(out, s)
+        if not fresh or stream is not None:     # a tensor made here belongs to the current stream
+            self._guard(out, s)
         return out
 
     def split_moments(self, values):

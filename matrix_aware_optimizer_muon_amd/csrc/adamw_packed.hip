@@ -182,24 +182,59 @@ struct Place {
   }
 };
 
+// 16 consecutive elements at element offset `at` of `base`, aligned to their
+// element only: the hardware takes 16-byte accesses at any such address.
+typedef float f32x4e_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef unsigned int u32x4h_t __attribute__((ext_vector_type(4), aligned(2)));
+template <bool F32>
+__device__ __forceinline__ void ld16(const void* base, int64_t at, float* x) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4e_t a = gld<f32x4e_t>(static_cast<const float*>(base) + at + 4 * q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[4 * q + k] = a[k];
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      unpack8_bf16(gld<u32x4h_t>(static_cast<const uint16_t*>(base) + at + 8 * q), x + 8 * q);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void st16(void* base, int64_t at, const float* x) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      gst<f32x4e_t>(static_cast<float*>(base) + at + 4 * q,
+                    f32x4e_t{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) gst<u32x4h_t>(static_cast<uint16_t*>(base) + at + 8 * q, pack8_bf16(x + 8 * q));
+  }
+}
+template <bool F32>
+__device__ __forceinline__ float ld1(const void* base, int64_t at) {
+  if constexpr (F32) return gld<float>(static_cast<const float*>(base) + at);
+  else return bf16_to_f32(gld<uint16_t>(static_cast<const uint16_t*>(base) + at));
+}
+template <bool F32>
+__device__ __forceinline__ void st1(void* base, int64_t at, float x) {
+  if constexpr (F32) gst(static_cast<float*>(base) + at, x);
+  else gst(static_cast<uint16_t*>(base) + at, f32_to_bf16(x));
+}
+
 // 16 elements from i on of param or grad; elements from n on are zero.
 template <bool F32>
 __device__ __forceinline__ void load_group(const PackedDev& d, const void* base, int64_t ld, int64_t i, float* x) {
   Place pl(d, i);
   if (d.vec && i + kPer <= d.n) {
-    const int64_t at = pl.at(d, ld);
-    ld8<F32>(base, at, x);
-    ld8<F32>(base, at + 8, x + 8);
+    ld16<F32>(base, pl.at(d, ld), x);
     return;
   }
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    x[e] = 0.f;
-    if (pl.i < d.n) {
-      const int64_t at = pl.at(d, ld);
-      if constexpr (F32) x[e] = gld<float>(static_cast<const float*>(base) + at);
-      else x[e] = bf16_to_f32(gld<uint16_t>(static_cast<const uint16_t*>(base) + at));
-    }
+    x[e] = pl.i < d.n ? ld1<F32>(base, pl.at(d, ld)) : 0.f;
     pl.next(d);
   }
 }
@@ -208,18 +243,12 @@ template <bool F32>
 __device__ __forceinline__ void store_group(const PackedDev& d, void* base, int64_t ld, int64_t i, const float* x) {
   Place pl(d, i);
   if (d.vec && i + kPer <= d.n) {
-    const int64_t at = pl.at(d, ld);
-    st8<F32>(base, at, x);
-    st8<F32>(base, at + 8, x + 8);
+    st16<F32>(base, pl.at(d, ld), x);
     return;
   }
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    if (pl.i < d.n) {
-      const int64_t at = pl.at(d, ld);
-      if constexpr (F32) gst(static_cast<float*>(base) + at, x[e]);
-      else gst(static_cast<uint16_t*>(base) + at, f32_to_bf16(x[e]));
-    }
+    if (pl.i < d.n) st1<F32>(base, pl.at(d, ld), x[e]);
     pl.next(d);
   }
 }
@@ -286,22 +315,20 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const PackedDev* __restr
   const int64_t i = tk.c0 + static_cast<int64_t>(threadIdx.x) * kPer;
   if (i >= d.blocks * kPackBlock) return;
   float m[kPer], v[kPer];
+  const int64_t at = d.value0 + i;
+  if (i + kPer <= d.n) {
+    ld16<F32>(values, at, m);
+    ld16<F32>(values, n_values + at, v);
+  } else {
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    m[e] = v[e] = 0.f;
-    if (i + e < d.n) {
-      const int64_t at = d.value0 + i + e;
-      if constexpr (F32) {
-        m[e] = gld<float>(static_cast<const float*>(values) + at);
-        v[e] = gld<float>(static_cast<const float*>(values) + n_values + at);
-      } else {
-        m[e] = bf16_to_f32(gld<uint16_t>(static_cast<const uint16_t*>(values) + at));
-        v[e] = bf16_to_f32(gld<uint16_t>(static_cast<const uint16_t*>(values) + n_values + at));
-      }
-      // a second moment below zero has no root: as in the update, NaN
-      if (!(v[e] >= 0.f)) m[e] = __uint_as_float(0x7FC00000u);
+    for (int e = 0; e < kPer; ++e) {
+      m[e] = i + e < d.n ? ld1<F32>(values, at + e) : 0.f;
+      v[e] = i + e < d.n ? ld1<F32>(values, n_values + at + e) : 0.f;
     }
   }
+  // a second moment below zero has no root: as in the update, NaN
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) m[e] = v[e] >= 0.f ? m[e] : __uint_as_float(0x7FC00000u);
   u32x4_t mc, vc;
   Scales s;
   const bool bad = encode<true>(m, v, 0, mc, vc, s);
@@ -319,17 +346,17 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const PackedDev* __res
   if (i >= d.n) return;
   float m[kPer], v[kPer];
   decode(gld<u32x4_t>(d.m + i), gld<u32x4_t>(d.v + i), load_scales(d, i), m, v);
+  const int64_t at = d.value0 + i;
+  if (i + kPer <= d.n) {
+    st16<F32>(values, at, m);
+    st16<F32>(values, n_values + at, v);
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < kPer; ++e)
     if (i + e < d.n) {
-      const int64_t at = d.value0 + i + e;
-      if constexpr (F32) {
-        gst(static_cast<float*>(values) + at, m[e]);
-        gst(static_cast<float*>(values) + n_values + at, v[e]);
-      } else {
-        gst(static_cast<uint16_t*>(values) + at, f32_to_bf16(m[e]));
-        gst(static_cast<uint16_t*>(values) + n_values + at, f32_to_bf16(v[e]));
-      }
+      st1<F32>(values, at + e, m[e]);
+      st1<F32>(values, n_values + at + e, v[e]);
     }
 }
 

@@ -186,7 +186,7 @@ std::vector<Buffer> buffers(const muon_tensor_t& t) {
   return out;
 }
 
-// Whether [p, p + bytes) touches a buffer of a tensor; `who` gets its name.
+// Whether [p, p + bytes) touches a buffer of a tensor; `who` (if asked for) gets its name.
 bool overlaps_tensors(const void* p, size_t bytes, const muon_tensor_t* ts, size_t n, std::string* who) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
   for (size_t i = 0; i < n; ++i)
@@ -773,7 +773,6 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
   auto al16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   for (size_t pi = 0; pi < plan.packed_tensors.size(); ++pi) {
     const muon_tensor_t& t = ts[plan.packed_tensors[pi]];
-    const int64_t es = t.dtype == MUON_F32 ? 4 : 2;
     PackedDev d;
     std::memset(&d, 0, sizeof(d));
     d.param = t.param;
@@ -788,8 +787,7 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.value0 = plan.packed_value0[pi];
     d.f32 = t.dtype == MUON_F32;
     d.flat = t.rows == 1 || (t.ld_param == t.cols && t.ld_grad == t.cols);
-    d.vec = al16(t.param) && al16(t.grad) &&
-            (d.flat || (t.cols % 16 == 0 && (t.ld_param * es) % 16 == 0 && (t.ld_grad * es) % 16 == 0));
+    d.vec = d.flat || t.cols % 16 == 0;
     d.tensor = uint32_t(plan.packed_tensors[pi]);
     d.lr_mult = t.lr_mult;
     std::memcpy(meta.data() + plan.off_packed_dev + pi * sizeof(PackedDev), &d, sizeof(d));
@@ -821,6 +819,7 @@ struct muon_handle_s {
   Plan plan;
   muon_hparams_t hp;
   std::vector<muon_tensor_t> tensors;
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // of the tensors' buffers, in order of address
   uint8_t* ws = nullptr;
   std::vector<uint8_t> meta;  // host copy of the uploaded descriptors (kept for the async copy)
   hipStream_t last_stream = nullptr;
@@ -1167,6 +1166,10 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   h->plan = std::move(plan);
   h->hp = *hp;
   h->tensors.assign(tensors, tensors + n_tensors);
+  for (const muon_tensor_t& t : h->tensors)
+    for (const Buffer& b : buffers(t))
+      h->spans.emplace_back(reinterpret_cast<uintptr_t>(b.p), reinterpret_cast<uintptr_t>(b.p) + b.bytes);
+  std::sort(h->spans.begin(), h->spans.end());
   h->ws = static_cast<uint8_t*>(workspace);
   h->meta = build_meta(h->plan, tensors, h->ws);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1314,10 +1317,14 @@ muon_status_t check_slot_block(muon_handle_t h, int32_t slot, int32_t block) {
 
 // A buffer that a call reads or writes beside the registered ones.
 muon_status_t check_apart(muon_handle_t h, const void* p, size_t bytes, const char* what) {
-  std::string who;
-  if (overlaps_tensors(p, bytes, h->tensors.data(), h->tensors.size(), &who))
-    return fail(MUON_ERR_ALIASING, std::string(what) + " overlaps " + who);
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p), wlo = reinterpret_cast<uintptr_t>(h->ws);
+  // the buffers do not overlap each other: the last one that begins below p + bytes ends last
+  const auto it = std::lower_bound(h->spans.begin(), h->spans.end(), std::make_pair(lo + bytes, uintptr_t(0)));
+  if (it != h->spans.begin() && std::prev(it)->second > lo) {
+    std::string who = "a registered tensor";
+    (void)overlaps_tensors(p, bytes, h->tensors.data(), h->tensors.size(), &who);
+    return fail(MUON_ERR_ALIASING, std::string(what) + " overlaps " + who);
+  }
   if (lo < wlo + h->plan.total && wlo < lo + bytes)
     return fail(MUON_ERR_ALIASING, std::string(what) + " overlaps the workspace");
   return MUON_OK;

@@ -204,7 +204,7 @@ struct PackedDev {
   int64_t value0;                      // elements of the packed tensors before this one
   int32_t f32;                         // param/grad float32 (else bf16)
   int32_t flat;                        // element i of param and grad lies at i
-  int32_t vec;                         // groups of 16 elements are contiguous and 16-byte aligned
+  int32_t vec;                         // groups of 16 elements are contiguous
   uint32_t tensor;                     // its place in the registered list (random words)
   float lr_mult;
   int32_t pad;
