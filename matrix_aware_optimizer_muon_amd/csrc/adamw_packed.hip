@@ -35,7 +35,7 @@
 //
 // A first moment that is not finite becomes e4m3's NaN and takes no part in
 // its block's scales; its second moment's byte is then without meaning.
-#include <type_traits>
+#include <cmath>
 
 #include "device_common.h"
 #include "muon_internal.h"
@@ -44,8 +44,17 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 16;                      // elements per thread: 16 lanes hold a block
-static_assert(kThreads * kPer == kPackChunk && kPackBlock == 16 * kPer, "a row of 16 lanes holds one block");
+// A thread takes 8 elements in groups of 16 bytes of the tensor (8 of bf16, 4
+// of float32), so that a wave's access is one run of 1 KB: at half that, 32
+// bytes apart, float32 values were written back in parts (unpacking 38.6 M
+// elements 113 us with streaming stores, 67 us without, XX as it is now).
+constexpr int kPer = 8;
+constexpr int kWave = 64 * kPer;              // elements per wave
+static_assert(kThreads * kPer == kPackChunk && kWave == 2 * kPackBlock, "a wave holds two blocks");
+template <bool F32> constexpr int kWidth = F32 ? 4 : 8;           // elements of a group
+template <bool F32> constexpr int kGroups = kPer / kWidth<F32>;   // groups of a thread
+constexpr int kWordGroup = 16;                // elements that share a hash
+template <int W> using codes_t = unsigned int __attribute__((ext_vector_type(W / 4)));
 
 constexpr uint32_t kGolden = 0x9E3779B9u;     // 2^32 over the golden ratio, odd
 constexpr uint32_t kRoot3 = 0xBB67AE85u;      // 2^32 (sqrt(3) - 1), odd
@@ -63,155 +72,192 @@ __device__ __forceinline__ uint32_t tensor_key(uint32_t seed_lo, uint32_t seed_h
   return mix(mix(mix(mix(seed_lo) + seed_hi) + t) + tensor);
 }
 
-// Maximum over the 16 lanes that hold a block (rotations within a DPP row).
-__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+// Maximum over the lanes that hold a block (W elements each): rotations within
+// the DPP rows of 16 lanes, the neighbouring row, and the other half.
+template <int W>
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x128, 0xF, 0xF, false)));
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x124, 0xF, 0xF, false)));
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x122, 0xF, 0xF, false)));
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x121, 0xF, 0xF, false)));
+  const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max(y[0], y[1]);
+  if constexpr (W == 4) {
+    const auto z = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(z[0], z[1]);
+  }
   return x;
+}
+
+// Streaming accesses: no buffer here is read again before the caches have
+// turned over.
+template <typename T>
+__device__ __forceinline__ T gld_nt(const void* p) {
+  return __builtin_nontemporal_load((const MUON_GLOBAL T*)p);
+}
+template <typename T>
+__device__ __forceinline__ void gst_nt(void* p, T v) {
+  __builtin_nontemporal_store(v, (MUON_GLOBAL T*)p);
+}
+
+// A descriptor held in scalar registers, read at once: left to itself the
+// compiler reads each field where it is used, one wait after another.
+__device__ __forceinline__ PackedDev load_desc(const PackedDev* p) {
+  PackedDev d = *p;
+  d.param = sreg_ptr(d.param);
+  d.grad = sreg_ptr(d.grad);
+  d.m = sreg_ptr(d.m);
+  d.v = sreg_ptr(d.v);
+  d.m_scales = sreg_ptr(d.m_scales);
+  d.v_scales = sreg_ptr(d.v_scales);
+  d.n = sreg_i64(d.n);
+  d.blocks = sreg_i64(d.blocks);
+  d.value0 = sreg_i64(d.value0);
+  return d;
 }
 
 struct Scales { uint32_t e, base; };
 
-// The scales of the block that holds element i.
-__device__ __forceinline__ const uint16_t* scale_at(const uint8_t* codes, int64_t blocks, int64_t i) {
-  return reinterpret_cast<const uint16_t*>(codes + blocks * kPackBlock) + i / kPackBlock;
-}
-__device__ __forceinline__ Scales load_scales(const PackedDev& d, int64_t i) {
+// One group's bytes and scales as they lie in memory.
+template <int W>
+struct Packed {
+  codes_t<W> m, v;
   Scales s;
-  s.e = max(static_cast<uint32_t>(gld<uint16_t>(scale_at(d.m, d.blocks, i))), kScaleLeast);
-  s.base = gld<uint16_t>(scale_at(d.v, d.blocks, i));
-  return s;
-}
-
-// 16 bytes of each moment to values.
-__device__ __forceinline__ void decode(const u32x4_t& mc, const u32x4_t& vc, const Scales& s, float* m, float* v) {
-  const float scale = __uint_as_float(s.e << 23);
-  const uint32_t vb = s.base << 20;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mc[q], scale, false);
-    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(mc[q], scale, true);
-    m[4 * q] = lo[0]; m[4 * q + 1] = lo[1]; m[4 * q + 2] = hi[0]; m[4 * q + 3] = hi[1];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t c = (vc[q] >> (8 * k)) & 0xFFu;
-      v[4 * q + k] = c ? __uint_as_float((c << 20) + vb) : 0.f;
+  template <typename I>
+  __device__ __forceinline__ void load(const PackedDev& d, I i) {
+    m = gld<codes_t<W>>(d.m + i);
+    v = gld<codes_t<W>>(d.v + i);
+    s.e = gld<uint16_t>(d.m_scales + i / kPackBlock);
+    s.base = gld<uint16_t>(d.v_scales + i / kPackBlock);
+  }
+  template <typename I>
+  __device__ __forceinline__ void store(const PackedDev& d, I i) const {
+    gst_nt(d.m + i, m);
+    gst_nt(d.v + i, v);
+    if ((threadIdx.x & (kPackBlock / W - 1)) == 0) {
+      gst(d.m_scales + i / kPackBlock, static_cast<uint16_t>(s.e));
+      gst(d.v_scales + i / kPackBlock, static_cast<uint16_t>(s.base));
     }
   }
-}
+  __device__ __forceinline__ void decode(float* mo, float* vo) const {
+    const float scale = __uint_as_float(max(s.e, kScaleLeast) << 23);   // a zero-filled buffer has no scales
+    const uint32_t vb = s.base << 20;
+#pragma unroll
+    for (int q = 0; q < W / 4; ++q) {
+      const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(m[q], scale, false);
+      const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(m[q], scale, true);
+      mo[4 * q] = lo[0]; mo[4 * q + 1] = lo[1]; mo[4 * q + 2] = hi[0]; mo[4 * q + 3] = hi[1];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t c = (v[q] >> (8 * k)) & 0xFFu;
+        vo[4 * q + k] = c ? __uint_as_float((c << 20) + vb) : 0.f;
+      }
+    }
+  }
+  // Values to bytes and scales; all lanes of a block call it together.  `word`
+  // is the random word of the first element; NEAREST rounds to nearest instead.
+  // Returns whether a first moment was not finite.
+  template <bool NEAREST>
+  __device__ __forceinline__ bool encode(const float* mi, float* vi, uint32_t word);
+};
 
-// Values of 16 elements to bytes; all lanes of a block call it together.
-// `word` is the random word of the first element; NEAREST rounds to nearest
-// instead.  Returns whether a first moment was not finite.
+template <int W>
 template <bool NEAREST>
-__device__ __forceinline__ bool encode(const float* m, const float* v, uint32_t word, u32x4_t& mc, u32x4_t& vc,
-                                       Scales& s) {
-  uint32_t vb[kPer];
+__device__ __forceinline__ bool Packed<W>::encode(const float* mi, float* vi, uint32_t word) {
   uint32_t mx = 0, vx = 0;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    vb[e] = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-    mx = max(mx, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-    vx = max(vx, vb[e]);
+  for (int e = 0; e < W; ++e) {
+    // the step's second moments carry no sign bit but a NaN's, which `odd` sees
+    if constexpr (NEAREST) vi[e] = fabsf(vi[e]);
+    mx = max(mx, __float_as_uint(mi[e]) & 0x7FFFFFFFu);
+    vx = max(vx, __float_as_uint(vi[e]));
   }
   const bool bad = mx >= kInf;
-  uint32_t m_top = row_max(mx), v_top = row_max(vx);
-  const bool odd = m_top >= kInf || v_top > kSecondMost;   // the same in the 16 lanes of a block
+  uint32_t m_top = block_max<W>(mx), v_top = block_max<W>(vx);
+  const bool odd = m_top >= kInf || v_top > kSecondMost;   // the same in all lanes of a block
   if (odd) {                       // leave non-finite elements out, bound the second moments
     mx = vx = 0;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const uint32_t a = __float_as_uint(m[e]) & 0x7FFFFFFFu;
-      vb[e] = a < kInf ? min(vb[e], kSecondMost) : 0u;
+    for (int e = 0; e < W; ++e) {
+      const uint32_t a = __float_as_uint(mi[e]) & 0x7FFFFFFFu;
+      const uint32_t b = a < kInf ? min(__float_as_uint(vi[e]), kSecondMost) : 0u;
       mx = max(mx, a < kInf ? a : 0u);
-      vx = max(vx, vb[e]);
+      vx = max(vx, b);
+      vi[e] = __uint_as_float(b);
     }
-    m_top = row_max(mx);
-    v_top = row_max(vx);
+    m_top = block_max<W>(mx);
+    v_top = block_max<W>(vx);
   }
   s.e = max(static_cast<int>((m_top + 0x1FFFFFu) >> 23) - 8, static_cast<int>(kScaleLeast));
   s.base = max(static_cast<int>((v_top + 0xFFFFFu) >> 20) - 255, 0);
   const float scale = __uint_as_float(s.e << 23);
+  const uint32_t below = s.base << 20;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < W / 4; ++q) {
     uint32_t cm = 0, cv = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int e = 4 * q + k;
-      uint32_t idx;
+      const uint32_t vb = __float_as_uint(vi[e]);
+      uint32_t add;            // what carries a share of the lower 20 bits into the index
       if constexpr (NEAREST) {
-        idx = (vb[e] + 0x7FFFFu + ((vb[e] >> 20) & 1u)) >> 20;
+        add = 0x7FFFFu + ((vb >> 20) & 1u);
       } else {
         const uint32_t w = word + static_cast<uint32_t>(e) * kGolden;
-        idx = (vb[e] + (w & 0xFFFFFu)) >> 20;
+        add = w & 0xFFFFFu;
         switch (k) {
-          case 0: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), m[e], w, scale, 0); break;
-          case 1: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), m[e], w, scale, 1); break;
-          case 2: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), m[e], w, scale, 2); break;
-          default: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), m[e], w, scale, 3);
+          case 0: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), mi[e], w, scale, 0); break;
+          case 1: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), mi[e], w, scale, 1); break;
+          case 2: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), mi[e], w, scale, 2); break;
+          default: cm = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(static_cast<int>(cm), mi[e], w, scale, 3);
         }
       }
       // at most 255, as base + 255 is not below the largest; at least 1 but for zero
-      const int c = max(static_cast<int>(idx - s.base), static_cast<int>(min(vb[e], 1u)));
+      const int c = max(static_cast<int>(vb + add - below) >> 20, static_cast<int>(min(vb, 1u)));
       cv |= static_cast<uint32_t>(c) << (8 * k);
     }
     if constexpr (NEAREST) {
       typedef short s16x2_t __attribute__((ext_vector_type(2)));
       s16x2_t h = {0, 0};
-      h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, m[4 * q], m[4 * q + 1], scale, false);
-      h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, m[4 * q + 2], m[4 * q + 3], scale, true);
+      h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, mi[4 * q], mi[4 * q + 1], scale, false);
+      h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, mi[4 * q + 2], mi[4 * q + 3], scale, true);
       cm = __builtin_bit_cast(uint32_t, h);
     }
-    mc[q] = cm;
-    vc[q] = cv;
+    m[q] = cm;
+    v[q] = cv;
   }
   return bad;
 }
 
-// Where an element of param or grad lies: at its index, or in the row that
-// holds it.
-struct Place {
-  int64_t i, r, c;
-  __device__ __forceinline__ Place(const PackedDev& d, int64_t i0) : i(i0), r(d.flat ? 0 : i0 / d.cols), c(i0 - r * d.cols) {}
-  __device__ __forceinline__ int64_t at(const PackedDev& d, int64_t ld) const { return d.flat ? i : r * ld + c; }
-  __device__ __forceinline__ void next(const PackedDev& d) {
-    ++i;
-    if (!d.flat && ++c == d.cols) { c = 0; ++r; }
-  }
-};
-
-// 16 consecutive elements at element offset `at` of `base`, aligned to their
-// element only: the hardware takes 16-byte accesses at any such address.
+// One group of param, grad or plain values, at element offset `at` of `base`:
+// 16 bytes, aligned to their element only (the hardware takes such accesses
+// at any address).
 typedef float f32x4e_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x4h_t __attribute__((ext_vector_type(4), aligned(2)));
-template <bool F32>
-__device__ __forceinline__ void ld16(const void* base, int64_t at, float* x) {
-  if constexpr (F32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4e_t a = gld<f32x4e_t>(static_cast<const float*>(base) + at + 4 * q);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[4 * q + k] = a[k];
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      unpack8_bf16(gld<u32x4h_t>(static_cast<const uint16_t*>(base) + at + 8 * q), x + 8 * q);
+template <bool F32> struct Raw;
+template <> struct Raw<true> {
+  f32x4_t q;
+  template <typename I>
+  __device__ __forceinline__ void load(const void* base, I at) {
+    q = gld_nt<f32x4e_t>(static_cast<const float*>(base) + at);
   }
-}
-template <bool F32>
-__device__ __forceinline__ void st16(void* base, int64_t at, const float* x) {
-  if constexpr (F32) {
+  __device__ __forceinline__ void values(float* x) const {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      gst<f32x4e_t>(static_cast<float*>(base) + at + 4 * q,
-                    f32x4e_t{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) gst<u32x4h_t>(static_cast<uint16_t*>(base) + at + 8 * q, pack8_bf16(x + 8 * q));
+    for (int e = 0; e < 4; ++e) x[e] = q[e];
   }
+};
+template <> struct Raw<false> {
+  u32x4_t q;
+  template <typename I>
+  __device__ __forceinline__ void load(const void* base, I at) {
+    q = gld_nt<u32x4h_t>(static_cast<const uint16_t*>(base) + at);
+  }
+  __device__ __forceinline__ void values(float* x) const { unpack8_bf16(q, x); }
+};
+template <bool F32, typename I>
+__device__ __forceinline__ void store_group(void* base, I at, const float* x) {
+  if constexpr (F32) gst_nt<f32x4e_t>(static_cast<float*>(base) + at, f32x4e_t{x[0], x[1], x[2], x[3]});
+  else gst_nt<u32x4h_t>(static_cast<uint16_t*>(base) + at, pack8_bf16(x));
 }
 template <bool F32>
 __device__ __forceinline__ float ld1(const void* base, int64_t at) {
@@ -224,115 +270,285 @@ __device__ __forceinline__ void st1(void* base, int64_t at, float x) {
   else gst(static_cast<uint16_t*>(base) + at, f32_to_bf16(x));
 }
 
-// 16 elements from i on of param or grad; elements from n on are zero.
+// First element, from the chunk's start, of this thread's group q: a wave's
+// groups of one q lie side by side.
 template <bool F32>
-__device__ __forceinline__ void load_group(const PackedDev& d, const void* base, int64_t ld, int64_t i, float* x) {
-  Place pl(d, i);
-  if (d.vec && i + kPer <= d.n) {
-    ld16<F32>(base, pl.at(d, ld), x);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    x[e] = pl.i < d.n ? ld1<F32>(base, pl.at(d, ld)) : 0.f;
-    pl.next(d);
-  }
+__device__ __forceinline__ uint32_t group_start(int q) {
+  return (threadIdx.x >> 6) * kWave + q * (64 * kWidth<F32>) + (threadIdx.x & 63) * kWidth<F32>;
 }
 
+// The descriptor with its buffers moved on to element c0, a chunk's first.
 template <bool F32>
-__device__ __forceinline__ void store_group(const PackedDev& d, void* base, int64_t ld, int64_t i, const float* x) {
-  Place pl(d, i);
-  if (d.vec && i + kPer <= d.n) {
-    st16<F32>(base, pl.at(d, ld), x);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    if (pl.i < d.n) st1<F32>(base, pl.at(d, ld), x[e]);
-    pl.next(d);
-  }
+__device__ __forceinline__ PackedDev chunk_desc(PackedDev d, int64_t c0) {
+  constexpr int es = F32 ? 4 : 2;
+  d.param = static_cast<char*>(d.param) + c0 * es;
+  d.grad = static_cast<const char*>(d.grad) + c0 * es;
+  d.m += c0;
+  d.v += c0;
+  d.m_scales += c0 / kPackBlock;
+  d.v_scales += c0 / kPackBlock;
+  return d;
 }
 
-__device__ __forceinline__ void store_packed(const PackedDev& d, int64_t i, const u32x4_t& mc, const u32x4_t& vc,
-                                             const Scales& s) {
-  gst(d.m + i, mc);
-  gst(d.v + i, vc);
-  if ((threadIdx.x & 15) == 0) {
-    gst(const_cast<uint16_t*>(scale_at(d.m, d.blocks, i)), static_cast<uint16_t>(s.e));
-    gst(const_cast<uint16_t*>(scale_at(d.v, d.blocks, i)), static_cast<uint16_t>(s.base));
+// What one step holds for all elements of a tensor.
+struct StepScalars {
+  float factor, beta1, beta2, c1, c2, inv_sqrt_bc2, eps, decay, step;
+  uint32_t key;
+  __device__ __forceinline__ StepScalars(const PackedDev& d, const PackedParams& p) {
+    const AdamParams& a = p.adam;
+    factor = a.factor ? gld<float>(a.factor) : 1.f;
+    const float lr = a.lr * d.lr_mult;
+    beta1 = a.beta1;
+    beta2 = a.beta2;
+    c1 = 1.f - a.beta1;
+    c2 = 1.f - a.beta2;
+    inv_sqrt_bc2 = a.state->inv_sqrt_bc2;
+    eps = a.eps;
+    decay = lr * a.weight_decay;
+    step = lr * a.state->inv_bc1;
+    key = tensor_key(p.seed_lo, p.seed_hi, a.state->t, d.tensor);
   }
-}
+};
 
-template <bool F32>
-__device__ __forceinline__ void step_group(const PackedDev& d, const PackedParams& p, int64_t i) {
-  const AdamParams& a = p.adam;
-  const u32x4_t mc0 = gld<u32x4_t>(d.m + i), vc0 = gld<u32x4_t>(d.v + i);
-  Scales s = load_scales(d, i);
-  float w[kPer], g[kPer], m[kPer], v[kPer];
-  load_group<F32>(d, d.param, d.ld_param, i, w);
-  load_group<F32>(d, d.grad, d.ld_grad, i, g);
-  decode(mc0, vc0, s, m, v);
-  const float factor = a.factor ? gld<float>(a.factor) : 1.f;
-  const float lr = a.lr * d.lr_mult, inv_bc1 = a.state->inv_bc1, inv_sqrt_bc2 = a.state->inv_sqrt_bc2;
-  const float c1 = 1.f - a.beta1, c2 = 1.f - a.beta2;
+// One group's update: w to the new weight, the moments to their new bytes.
+// `at`: the group's first element.  Returns whether a first moment is not
+// finite.
+// PRECISE: sqrtf and division as the language has them.  Otherwise the
+// hardware's own square root and reciprocal, each within one unit in the
+// last place; that square root takes denormal numbers as zero, so it is used
+// where 2^-63, the largest root lost, leaves eps as it is (launch_adamw_packed).
+template <bool PRECISE, int W>
+__device__ __forceinline__ bool update_group(const StepScalars& k, Packed<W>& pk, float* w, const float* g,
+                                             uint32_t word) {
+  float m[W], v[W];
+  pk.decode(m, v);
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
+  for (int e = 0; e < W; ++e) {
 #pragma clang fp contract(off)
-    const float ge = g[e] * factor;
-    m[e] = a.beta1 * m[e] + c1 * ge;
-    v[e] = a.beta2 * v[e] + (c2 * ge) * ge;
+    const float ge = g[e] * k.factor;
+    m[e] = k.beta1 * m[e] + k.c1 * ge;
+    v[e] = k.beta2 * v[e] + (k.c2 * ge) * ge;
   }
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const float den = sqrtf(v[e]) * inv_sqrt_bc2 + a.eps;
-    w[e] = w[e] - lr * a.weight_decay * w[e] - lr * (m[e] * inv_bc1 / den);
+  for (int e = 0; e < W; ++e) {
+    const float root = PRECISE ? sqrtf(v[e]) : __builtin_amdgcn_sqrtf(v[e]);
+    const float den = fmaf(root, k.inv_sqrt_bc2, k.eps);
+    const float term = PRECISE ? m[e] / den : m[e] * __builtin_amdgcn_rcpf(den);
+    w[e] = fmaf(-k.step, term, fmaf(-k.decay, w[e], w[e]));
   }
-  store_group<F32>(d, d.param, d.ld_param, i, w);
-  const uint32_t key = tensor_key(p.seed_lo, p.seed_hi, a.state->t, d.tensor);
-  u32x4_t mc, vc;
-  const bool bad = encode<false>(m, v, mix(key + static_cast<uint32_t>(i / kPer)), mc, vc, s);
-  store_packed(d, i, mc, vc, s);
-  if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(a.flags, 1u);
+  return pk.template encode<false>(m, v, word);
 }
 
-__global__ __launch_bounds__(kThreads) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
-                                                                const PackedTask* __restrict__ tasks,
-                                                                PackedParams p) {
-  const PackedTask tk = tasks[blockIdx.x];
-  const PackedDev& d = tensors[tk.tensor];
-  const int64_t i = tk.c0 + static_cast<int64_t>(threadIdx.x) * kPer;
-  if (i >= d.blocks * kPackBlock) return;      // whole blocks: the 16 lanes of one stay or leave together
-  if (d.f32) step_group<true>(d, p, i);
-  else step_group<false>(d, p, i);
+// The random word of element i of a tensor.
+__device__ __forceinline__ uint32_t random_word(uint32_t key, int64_t i) {
+  return mix(key + static_cast<uint32_t>(i / kWordGroup)) + static_cast<uint32_t>(i % kWordGroup) * kGolden;
 }
+
+// A chunk that lies inside its tensor, contiguous in memory: one base for the
+// block and 32-bit offsets for the lanes, every load before the first use of
+// one.
+template <bool F32, bool PRECISE>
+__device__ __forceinline__ bool step_whole_chunk(const PackedDev& d, const PackedParams& p, int64_t c0) {
+  constexpr int W = kWidth<F32>, G = kGroups<F32>;
+  const PackedDev c = chunk_desc<F32>(d, c0);
+  Packed<W> pk[G];
+  Raw<F32> wr[G], gr[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const uint32_t i = group_start<F32>(q);
+    pk[q].load(c, i);
+    wr[q].load(c.param, i);
+    gr[q].load(c.grad, i);
+  }
+  const StepScalars k(d, p);
+  const uint32_t key = k.key + static_cast<uint32_t>(c0 / kWordGroup);
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const uint32_t i = group_start<F32>(q);
+    float w[W], g[W];
+    wr[q].values(w);
+    gr[q].values(g);
+    bad |= update_group<PRECISE, W>(k, pk[q], w, g, random_word(key, i));
+    store_group<F32>(c.param, i, w);
+    pk[q].store(c, i);
+  }
+  return bad;
+}
+
+// A contiguous tensor's last chunk, of which `left` elements are its own.
+template <bool F32, bool PRECISE>
+__device__ __forceinline__ bool step_last_chunk(const PackedDev& d, const PackedParams& p, int64_t c0, uint32_t left) {
+  constexpr int W = kWidth<F32>, G = kGroups<F32>;
+  const PackedDev c = chunk_desc<F32>(d, c0);
+  const uint32_t blocks_left = (left + kPackBlock - 1) / kPackBlock * kPackBlock;
+  const StepScalars k(d, p);
+  const uint32_t key = k.key + static_cast<uint32_t>(c0 / kWordGroup);
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const uint32_t i = group_start<F32>(q);
+    if (i >= blocks_left) break;               // whole blocks: the lanes of one stay or leave together
+    Packed<W> pk;
+    pk.load(c, i);
+    float w[W], g[W];
+    if (i + W <= left) {
+      Raw<F32> wr, gr;
+      wr.load(c.param, i);
+      gr.load(c.grad, i);
+      wr.values(w);
+      gr.values(g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        w[e] = i + e < left ? ld1<F32>(c.param, i + e) : 0.f;
+        g[e] = i + e < left ? ld1<F32>(c.grad, i + e) : 0.f;
+      }
+    }
+    bad |= update_group<PRECISE, W>(k, pk, w, g, random_word(key, i));
+    if (i + W <= left) {
+      store_group<F32>(c.param, i, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if (i + e < left) st1<F32>(c.param, i + e, w[e]);
+    }
+    pk.store(c, i);
+  }
+  return bad;
+}
+
+// Where an element of a tensor with gaps between its rows lies.
+struct Place {
+  int64_t i, r, c, cols;
+  __device__ __forceinline__ Place(const PackedDev& d, int64_t i0) : i(i0), r(i0 / d.cols), c(i0 - r * d.cols), cols(d.cols) {}
+  __device__ __forceinline__ int64_t at(int64_t ld) const { return r * ld + c; }
+  __device__ __forceinline__ void next() {
+    ++i;
+    if (++c == cols) { c = 0; ++r; }
+  }
+};
+
+// A chunk of a tensor with gaps between its rows: group by group where rows
+// hold whole groups, else one element after another.
+template <bool F32, bool PRECISE>
+__device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const PackedParams& p, int64_t c0) {
+  constexpr int W = kWidth<F32>, G = kGroups<F32>;
+  const StepScalars k(d, p);
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int64_t i = c0 + group_start<F32>(q);
+    if (i >= d.blocks * kPackBlock) break;     // whole blocks: the lanes of one stay or leave together
+    Packed<W> pk;
+    pk.load(d, i);
+    float w[W], g[W];
+    const Place pl(d, i);
+    const bool whole = d.vec && i + W <= d.n;
+    if (whole) {
+      Raw<F32> wr, gr;
+      wr.load(d.param, pl.at(d.ld_param));
+      gr.load(d.grad, pl.at(d.ld_grad));
+      wr.values(w);
+      gr.values(g);
+    } else {
+      Place x = pl;
+#pragma unroll
+      for (int e = 0; e < W; ++e, x.next()) {
+        w[e] = x.i < d.n ? ld1<F32>(d.param, x.at(d.ld_param)) : 0.f;
+        g[e] = x.i < d.n ? ld1<F32>(d.grad, x.at(d.ld_grad)) : 0.f;
+      }
+    }
+    bad |= update_group<PRECISE, W>(k, pk, w, g, random_word(k.key, i));
+    if (whole) {
+      store_group<F32>(d.param, pl.at(d.ld_param), w);
+    } else {
+      Place x = pl;
+#pragma unroll
+      for (int e = 0; e < W; ++e, x.next())
+        if (x.i < d.n) st1<F32>(d.param, x.at(d.ld_param), w[e]);
+    }
+    pk.store(d, i);
+  }
+  return bad;
+}
+
+// Tensors with gaps between their rows (ROWS) have a kernel of their own: the
+// other one then needs 64 registers, not 78, for 8 waves a SIMD instead of 6
+// (82 M bf16 elements 128 against 137 us).
+template <bool F32, bool PRECISE, bool ROWS>
+__global__ __launch_bounds__(kThreads, 8) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
+                                                                              const PackedTask* __restrict__ tasks,
+                                                                              PackedParams p) {
+  const PackedTask tk = tasks[blockIdx.x];
+  const PackedDev d = load_desc(tensors + tk.tensor);
+  bool bad;
+  if constexpr (ROWS) {
+    bad = step_rows_chunk<F32, PRECISE>(d, p, tk.c0);
+  } else {
+    const int64_t left = d.n - tk.c0;
+    if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, tk.c0);
+    else bad = step_last_chunk<F32, PRECISE>(d, p, tk.c0, static_cast<uint32_t>(left));
+  }
+  if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(p.adam.flags, 1u);
+}
+
+// A chunk's plain values: first moments at `first`, second ones at `second`.
+template <bool F32>
+struct ValueRuns {
+  char *first, *second;
+  __device__ __forceinline__ ValueRuns(const void* values, int64_t n_values, const PackedDev& d, int64_t c0) {
+    constexpr int es = F32 ? 4 : 2;
+    first = static_cast<char*>(const_cast<void*>(values)) + (d.value0 + c0) * es;
+    second = first + n_values * es;
+  }
+};
 
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const PackedDev* __restrict__ tensors,
                                                         const PackedTask* __restrict__ tasks, const void* values,
                                                         int64_t n_values, uint32_t* flags) {
+  constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedTask tk = tasks[blockIdx.x];
-  const PackedDev& d = tensors[tk.tensor];
-  const int64_t i = tk.c0 + static_cast<int64_t>(threadIdx.x) * kPer;
-  if (i >= d.blocks * kPackBlock) return;
-  float m[kPer], v[kPer];
-  const int64_t at = d.value0 + i;
-  if (i + kPer <= d.n) {
-    ld16<F32>(values, at, m);
-    ld16<F32>(values, n_values + at, v);
+  const PackedDev d = load_desc(tensors + tk.tensor);
+  const ValueRuns<F32> runs(values, n_values, d, tk.c0);
+  const int64_t left = d.n - tk.c0, blocks_left = d.blocks * kPackBlock - tk.c0;
+  float m[G][W], v[G][W];
+  if (left >= kPackChunk) {
+    Raw<F32> mr[G], vr[G];
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      mr[q].load(runs.first, group_start<F32>(q));
+      vr[q].load(runs.second, group_start<F32>(q));
+    }
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      mr[q].values(m[q]);
+      vr[q].values(v[q]);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      m[e] = i + e < d.n ? ld1<F32>(values, at + e) : 0.f;
-      v[e] = i + e < d.n ? ld1<F32>(values, n_values + at + e) : 0.f;
-    }
-  }
-  // a second moment below zero has no root: as in the update, NaN
+    for (int q = 0; q < G; ++q)
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) m[e] = v[e] >= 0.f ? m[e] : __uint_as_float(0x7FC00000u);
-  u32x4_t mc, vc;
-  Scales s;
-  const bool bad = encode<true>(m, v, 0, mc, vc, s);
-  store_packed(d, i, mc, vc, s);
+      for (int e = 0; e < W; ++e) {
+        const uint32_t i = group_start<F32>(q) + e;
+        m[q][e] = i < left ? ld1<F32>(runs.first, i) : 0.f;
+        v[q][e] = i < left ? ld1<F32>(runs.second, i) : 0.f;
+      }
+  }
+  const PackedDev c = chunk_desc<F32>(d, tk.c0);
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const uint32_t i = group_start<F32>(q);
+    if (i >= blocks_left) break;               // whole blocks: the lanes of one stay or leave together
+    // a second moment below zero has no root: as in the update, NaN
+#pragma unroll
+    for (int e = 0; e < W; ++e) m[q][e] = v[q][e] >= 0.f ? m[q][e] : __uint_as_float(0x7FC00000u);
+    Packed<W> pk;
+    bad |= pk.template encode<true>(m[q], v[q], 0);
+    pk.store(c, i);
+  }
   if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(flags, 1u);
 }
 
@@ -340,32 +556,68 @@ template <bool F32>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const PackedDev* __restrict__ tensors,
                                                           const PackedTask* __restrict__ tasks, void* values,
                                                           int64_t n_values) {
+  constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedTask tk = tasks[blockIdx.x];
-  const PackedDev& d = tensors[tk.tensor];
-  const int64_t i = tk.c0 + static_cast<int64_t>(threadIdx.x) * kPer;
-  if (i >= d.n) return;
-  float m[kPer], v[kPer];
-  decode(gld<u32x4_t>(d.m + i), gld<u32x4_t>(d.v + i), load_scales(d, i), m, v);
-  const int64_t at = d.value0 + i;
-  if (i + kPer <= d.n) {
-    st16<F32>(values, at, m);
-    st16<F32>(values, n_values + at, v);
+  const PackedDev d = load_desc(tensors + tk.tensor);
+  const ValueRuns<F32> runs(values, n_values, d, tk.c0);
+  const PackedDev c = chunk_desc<F32>(d, tk.c0);
+  const int64_t left = d.n - tk.c0;
+  Packed<W> pk[G];
+  if (left >= kPackChunk) {
+#pragma unroll
+    for (int q = 0; q < G; ++q) pk[q].load(c, group_start<F32>(q));
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      float m[W], v[W];
+      pk[q].decode(m, v);
+      store_group<F32>(runs.first, group_start<F32>(q), m);
+      store_group<F32>(runs.second, group_start<F32>(q), v);
+    }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (i + e < d.n) {
-      st1<F32>(values, at + e, m[e]);
-      st1<F32>(values, n_values + at + e, v[e]);
+  for (int q = 0; q < G; ++q) {
+    const uint32_t i = group_start<F32>(q);
+    if (i >= left) break;
+    pk[q].load(c, i);
+    float m[W], v[W];
+    pk[q].decode(m, v);
+    if (i + W <= left) {
+      store_group<F32>(runs.first, i, m);
+      store_group<F32>(runs.second, i, v);
+      continue;
     }
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (i + e < left) {
+        st1<F32>(runs.first, i + e, m[e]);
+        st1<F32>(runs.second, i + e, v[e]);
+      }
+  }
 }
 
 }  // namespace
 
-hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, int n_tasks, const PackedParams& p,
-                               hipStream_t s) {
-  if (n_tasks <= 0) return hipSuccess;
-  adamw_packed_kernel<<<n_tasks, kThreads, 0, s>>>(tensors, tasks, p);
+namespace {
+template <bool F32, bool ROWS>
+const PackedTask* launch_step(bool precise, const PackedDev* tensors, const PackedTask* tasks, int n,
+                              const PackedParams& p, hipStream_t s) {
+  if (n > 0) {
+    if (precise) adamw_packed_kernel<F32, true, ROWS><<<n, kThreads, 0, s>>>(tensors, tasks, p);
+    else adamw_packed_kernel<F32, false, ROWS><<<n, kThreads, 0, s>>>(tensors, tasks, p);
+  }
+  return tasks + n;
+}
+}  // namespace
+
+hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, const int* n,
+                               const PackedParams& p, hipStream_t s) {
+  // a root below 2^-63 times at most 1 / sqrt(1 - b2) stays under half a unit (2^-24) of eps
+  const bool precise = !(p.adam.eps * std::sqrt(1.f - p.adam.beta2) >= 0x1p-39f);
+  tasks = launch_step<false, false>(precise, tensors, tasks, n[0], p, s);
+  tasks = launch_step<false, true>(precise, tensors, tasks, n[1], p, s);
+  tasks = launch_step<true, false>(precise, tensors, tasks, n[2], p, s);
+  (void)launch_step<true, true>(precise, tensors, tasks, n[3], p, s);
   return hipGetLastError();
 }
 

@@ -144,6 +144,7 @@ struct Plan {
   std::vector<int> packed_tensors;   // kind-ADAMW tensors with 8-bit moments, in tensor order
   std::vector<int64_t> packed_value0;  // elements of the packed tensors before each
   std::vector<PackedTask> packed_tasks;
+  int packed_kind[kPackKinds] = {};  // packed tasks of each kind of tensor (launch_adamw_packed)
   int64_t packed_elems = 0;
   size_t off_packed_dev = 0, off_packed_tasks = 0;
   std::vector<int64_t> norm_chunk0;  // per tensor: gradient-norm chunks of the tensors before it
@@ -169,6 +170,9 @@ float shape_scale(int64_t rows, int64_t cols, int mode) {
     default: return 1.f;
   }
 }
+
+// Whether element (i, j) of param and grad lies at i * cols + j.
+bool gapless(const muon_tensor_t& t) { return t.rows == 1 || (t.ld_param == t.cols && t.ld_grad == t.cols); }
 
 bool packed(const muon_tensor_t& t) { return t.kind == MUON_KIND_ADAMW && t.state_bits == 8; }
 
@@ -471,6 +475,7 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   }
   plan.apply_bf16 = int(plan.apply.size());
   plan.apply.insert(plan.apply.end(), apply_f32.begin(), apply_f32.end());
+  std::vector<PackedTask> packed_by_kind[kPackKinds];
   // AdamW tensors: rows of `len` elements in chunks of kAdamChunk; a fully
   // contiguous tensor is one row of rows*cols elements
   for (int32_t i = 0; i < n; ++i) {
@@ -480,7 +485,8 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
       const int pi = int(plan.packed_tensors.size());
       plan.packed_tensors.push_back(i);
       plan.packed_value0.push_back(plan.packed_elems);
-      for (int64_t c0 = 0; c0 < t.rows * t.cols; c0 += kPackChunk) plan.packed_tasks.push_back({pi, 0, c0});
+      std::vector<PackedTask>& dst = packed_by_kind[(t.dtype == MUON_F32 ? 2 : 0) + (gapless(t) ? 0 : 1)];
+      for (int64_t c0 = 0; c0 < t.rows * t.cols; c0 += kPackChunk) dst.push_back({pi, 0, c0});
       plan.packed_elems += t.rows * t.cols;
       continue;
     }
@@ -490,6 +496,10 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
     const int64_t nrows = flat ? 1 : t.rows, len = flat ? t.rows * t.cols : t.cols;
     for (int64_t r = 0; r < nrows; ++r)
       for (int64_t c0 = 0; c0 < len; c0 += kAdamChunk) plan.adam_tasks.push_back({ai, int32_t(r), c0});
+  }
+  for (int k = 0; k < kPackKinds; ++k) {
+    plan.packed_kind[k] = int(packed_by_kind[k].size());
+    plan.packed_tasks.insert(plan.packed_tasks.end(), packed_by_kind[k].begin(), packed_by_kind[k].end());
   }
   plan.with_norm = with_norm;
   for (int32_t i = 0; i < n; ++i) {
@@ -784,10 +794,11 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.n = t.rows * t.cols;
     d.cols = t.cols;
     d.blocks = packed_blocks(d.n);
+    d.m_scales = reinterpret_cast<uint16_t*>(d.m + d.blocks * kPackBlock);
+    d.v_scales = reinterpret_cast<uint16_t*>(d.v + d.blocks * kPackBlock);
     d.value0 = plan.packed_value0[pi];
     d.f32 = t.dtype == MUON_F32;
-    d.flat = t.rows == 1 || (t.ld_param == t.cols && t.ld_grad == t.cols);
-    d.vec = d.flat || t.cols % 16 == 0;
+    d.vec = gapless(t) || t.cols % 8 == 0;
     d.tensor = uint32_t(plan.packed_tensors[pi]);
     d.lr_mult = t.lr_mult;
     std::memcpy(meta.data() + plan.off_packed_dev + pi * sizeof(PackedDev), &d, sizeof(d));
@@ -896,7 +907,7 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     if (e == hipSuccess && !plan.packed_tasks.empty())
       e = launch_adamw_packed(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
                               reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
-                              int(plan.packed_tasks.size()),
+                              plan.packed_kind,
                               PackedParams{ap, uint32_t(h->rounding_seed), uint32_t(h->rounding_seed >> 32)}, as);
     if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("adamw launch: ") + hipGetErrorString(e));
     return MUON_OK;

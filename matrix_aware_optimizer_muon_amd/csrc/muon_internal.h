@@ -191,23 +191,22 @@ struct AdamParams {
 // scale a block behind the bytes of all blocks (adamw_packed.hip has the
 // formats).
 constexpr int kPackBlock = 256;
-constexpr int kPackChunk = 4096;       // elements per thread block (256 threads x 16)
+constexpr int kPackChunk = 2048;       // elements per thread block (256 threads x 8)
 constexpr int64_t kPackMaxElems = int64_t(1) << 35;   // element / 16 fits the 32-bit counter of the random words
 inline int64_t packed_blocks(int64_t n) { return (n + kPackBlock - 1) / kPackBlock; }
 inline int64_t packed_bytes(int64_t n) { return packed_blocks(n) * (kPackBlock + 2); }
 struct PackedDev {
   void* param; const void* grad;
-  uint8_t* m; uint8_t* v;              // codes; the scales are at + kPackBlock * blocks
+  uint8_t* m; uint8_t* v;              // bytes of the elements, whole blocks
+  uint16_t* m_scales; uint16_t* v_scales;   // one a block, behind the bytes
   int64_t ld_param, ld_grad;           // elements between rows
   int64_t n, cols;                     // elements in all, and per row
   int64_t blocks;
   int64_t value0;                      // elements of the packed tensors before this one
   int32_t f32;                         // param/grad float32 (else bf16)
-  int32_t flat;                        // element i of param and grad lies at i
-  int32_t vec;                         // groups of 16 elements are contiguous
+  int32_t vec;                         // groups of 8 elements are contiguous
   uint32_t tensor;                     // its place in the registered list (random words)
   float lr_mult;
-  int32_t pad;
 };
 struct PackedTask { int32_t tensor, pad; int64_t c0; };
 struct PackedParams {
@@ -250,7 +249,10 @@ hipError_t launch_adamw(const AdamDev* tensors, const AdamTask* tasks, int n_tas
 
 // Weak: the planner also links, and plans, without the kernels below.
 #define MUON_WEAK __attribute__((weak))
-MUON_WEAK hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
+// n: chunks of each kind of tensor, in the order of the tasks: bf16 without
+// and with gaps between rows, float32 without and with
+constexpr int kPackKinds = 4;
+MUON_WEAK hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, const int* n,
                                          const PackedParams& p, hipStream_t s);
 // values: n_values first moments, then n_values second ones, float32 or bf16
 MUON_WEAK hipError_t launch_pack_moments(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
