@@ -379,6 +379,12 @@ class MuonStep:
         return stream if stream is not None else torch.cuda.current_stream(self.device)
 
     def _stream(self, stream):
+        """The hipStream_t of `stream`, or of torch's current one (asked for
+        as a number where torch has that: a Stream object takes 1.5 us)."""
+        if stream is None:
+            raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:
+                return ctypes.c_void_p(raw(self.device.index))
         return ctypes.c_void_p(self._torch_stream(stream).cuda_stream)
 
     def _here(self):
@@ -493,11 +499,11 @@ class MuonStep:
         bfloat16 tensor [2, packed_elements()]: the first moments of all packed
         tensors one after another, then the second ones (round to nearest)."""
         dt = self._check_values(values, "values")
-        s = self._torch_stream(stream)
+        s = self._stream(stream)
         with self._here():
-            self._check(self._lib.muon_pack_moments(self._h, ctypes.c_void_p(values.data_ptr()), dt,
-                                               ctypes.c_void_p(s.cuda_stream)))
-        self._guard(values, s)
+            self._check(self._lib.muon_pack_moments(self._h, ctypes.c_void_p(values.data_ptr()), dt, s))
+        if stream is not None:
+            self._guard(values, stream)
 
     def unpack_moments(self, dtype=None, out=None, stream=None):
         """The values of every packed moment, exactly, as a tensor
@@ -505,18 +511,16 @@ class MuonStep:
         float32), laid out as pack_moments takes it; into `out` if given.
         split_moments cuts it into the tensors' own."""
         torch = _torch()
-        fresh = out is None
-        if fresh:
+        if out is None:
             out = torch.empty((2, self._packed_elements), dtype=dtype or torch.float32, device=self.device)
         elif dtype is not None and dtype != out.dtype:
             raise ValueError("out is not of the dtype asked for")
         dt = self._check_values(out, "out")
-        s = self._torch_stream(stream)
+        s = self._stream(stream)
         with self._here():
-            self._check(self._lib.muon_unpack_moments(self._h, ctypes.c_void_p(out.data_ptr()), dt,
-                                                 ctypes.c_void_p(s.cuda_stream)))
-        if not fresh or stream is not None:     # a tensor made here belongs to the current stream
-            self._guard(out, s)
+            self._check(self._lib.muon_unpack_moments(self._h, ctypes.c_void_p(out.data_ptr()), dt, s))
+        if stream is not None:
+            self._guard(out, stream)
         return out
 
     def split_moments(self, values):

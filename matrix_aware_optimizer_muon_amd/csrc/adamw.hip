@@ -23,12 +23,7 @@ constexpr int kThreads = 256;
 
 __global__ void adam_tick_kernel(AdamState* st, float beta1, float beta2) {
   if (threadIdx.x != 0 || blockIdx.x != 0) return;
-  const uint32_t t = st->t + 1;
-  st->t = t;
-  const double bc1 = 1.0 - pow(double(beta1), double(t));
-  const double bc2 = 1.0 - pow(double(beta2), double(t));
-  st->inv_bc1 = float(1.0 / bc1);
-  st->inv_sqrt_bc2 = float(1.0 / sqrt(bc2));
+  adam_advance(st, beta1, beta2);
 }
 
 __global__ void adam_set_kernel(AdamState* st, uint32_t t) {

@@ -56,21 +56,9 @@ template <bool F32> constexpr int kGroups = kPer / kWidth<F32>;   // groups of a
 constexpr int kWordGroup = 16;                // elements that share a hash
 template <int W> using codes_t = unsigned int __attribute__((ext_vector_type(W / 4)));
 
-constexpr uint32_t kGolden = 0x9E3779B9u;     // 2^32 over the golden ratio, odd
-constexpr uint32_t kRoot3 = 0xBB67AE85u;      // 2^32 (sqrt(3) - 1), odd
 constexpr uint32_t kInf = 0x7F800000u;
 constexpr uint32_t kSecondMost = 0x7F700000u; // 1.875 * 2^127, the largest second moment a byte stands for
 constexpr uint32_t kScaleLeast = 9;           // keeps e4m3's smallest value times the scale exact in bf16
-
-// Two rounds of xor-shift and multiplication: a bijection of 32 bits.
-__device__ __forceinline__ uint32_t mix(uint32_t x) {
-  x = (x ^ (x >> 16)) * kGolden;
-  x = (x ^ (x >> 15)) * kRoot3;
-  return x ^ (x >> 16);
-}
-__device__ __forceinline__ uint32_t tensor_key(uint32_t seed_lo, uint32_t seed_hi, uint32_t t, uint32_t tensor) {
-  return mix(mix(mix(mix(seed_lo) + seed_hi) + t) + tensor);
-}
 
 // Maximum over the lanes that hold a block (W elements each): rotations within
 // the DPP rows of 16 lanes, the neighbouring row, and the other half.
@@ -294,7 +282,8 @@ __device__ __forceinline__ PackedDev chunk_desc(PackedDev d, int64_t c0) {
 struct StepScalars {
   float factor, beta1, beta2, c1, c2, inv_sqrt_bc2, eps, decay, step;
   uint32_t key;
-  __device__ __forceinline__ StepScalars(const PackedDev& d, const PackedParams& p) {
+  __device__ __forceinline__ StepScalars(const PackedDev& d, const PackedParams& p, const AdamBias& bias,
+                                         uint32_t tensor_key) {
     const AdamParams& a = p.adam;
     factor = a.factor ? gld<float>(a.factor) : 1.f;
     const float lr = a.lr * d.lr_mult;
@@ -302,11 +291,11 @@ struct StepScalars {
     beta2 = a.beta2;
     c1 = 1.f - a.beta1;
     c2 = 1.f - a.beta2;
-    inv_sqrt_bc2 = a.state->inv_sqrt_bc2;
+    inv_sqrt_bc2 = bias.inv_sqrt_bc2;
     eps = a.eps;
     decay = lr * a.weight_decay;
-    step = lr * a.state->inv_bc1;
-    key = tensor_key(p.seed_lo, p.seed_hi, a.state->t, d.tensor);
+    step = lr * bias.inv_bc1;
+    key = tensor_key;
   }
 };
 
@@ -347,8 +336,9 @@ __device__ __forceinline__ uint32_t random_word(uint32_t key, int64_t i) {
 // A chunk that lies inside its tensor, contiguous in memory: one base for the
 // block and 32-bit offsets for the lanes, every load before the first use of
 // one.
-template <bool F32, bool PRECISE>
-__device__ __forceinline__ bool step_whole_chunk(const PackedDev& d, const PackedParams& p, int64_t c0) {
+template <bool F32, bool PRECISE, typename Begin>
+__device__ __forceinline__ bool step_whole_chunk(const PackedDev& d, const PackedParams& p, const Begin& begin,
+                                                 int64_t c0) {
   constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedDev c = chunk_desc<F32>(d, c0);
   Packed<W> pk[G];
@@ -360,7 +350,7 @@ __device__ __forceinline__ bool step_whole_chunk(const PackedDev& d, const Packe
     wr[q].load(c.param, i);
     gr[q].load(c.grad, i);
   }
-  const StepScalars k(d, p);
+  const StepScalars k = begin(d, p);
   const uint32_t key = k.key + static_cast<uint32_t>(c0 / kWordGroup);
   bool bad = false;
 #pragma unroll
@@ -377,12 +367,13 @@ __device__ __forceinline__ bool step_whole_chunk(const PackedDev& d, const Packe
 }
 
 // A contiguous tensor's last chunk, of which `left` elements are its own.
-template <bool F32, bool PRECISE>
-__device__ __forceinline__ bool step_last_chunk(const PackedDev& d, const PackedParams& p, int64_t c0, uint32_t left) {
+template <bool F32, bool PRECISE, typename Begin>
+__device__ __forceinline__ bool step_last_chunk(const PackedDev& d, const PackedParams& p, const Begin& begin,
+                                                int64_t c0, uint32_t left) {
   constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedDev c = chunk_desc<F32>(d, c0);
   const uint32_t blocks_left = (left + kPackBlock - 1) / kPackBlock * kPackBlock;
-  const StepScalars k(d, p);
+  const StepScalars k = begin(d, p);
   const uint32_t key = k.key + static_cast<uint32_t>(c0 / kWordGroup);
   bool bad = false;
 #pragma unroll
@@ -431,10 +422,11 @@ struct Place {
 
 // A chunk of a tensor with gaps between its rows: group by group where rows
 // hold whole groups, else one element after another.
-template <bool F32, bool PRECISE>
-__device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const PackedParams& p, int64_t c0) {
+template <bool F32, bool PRECISE, typename Begin>
+__device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const PackedParams& p, const Begin& begin,
+                                                 int64_t c0) {
   constexpr int W = kWidth<F32>, G = kGroups<F32>;
-  const StepScalars k(d, p);
+  const StepScalars k = begin(d, p);
   bool bad = false;
 #pragma unroll
   for (int q = 0; q < G; ++q) {
@@ -476,21 +468,36 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
 // Tensors with gaps between their rows (ROWS) have a kernel of their own: the
 // other one then needs 64 registers, not 78, for 8 waves a SIMD instead of 6
 // (82 M bf16 elements 128 against 137 us).
-template <bool F32, bool PRECISE, bool ROWS>
-__global__ __launch_bounds__(kThreads, 8) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
-                                                                              const PackedTask* __restrict__ tasks,
-                                                                              PackedParams p) {
+// BEGINS: no launch has advanced the step count before this one.  Every wave
+// takes the next step's bias corrections itself, while its loads are under
+// way, and the last block advances the count (launch_adamw_packed).
+template <bool F32, bool PRECISE, bool ROWS, bool BEGINS>
+__global__ __launch_bounds__(kThreads, BEGINS ? 4 : 8) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
+                                                                                const PackedTask* __restrict__ tasks,
+                                                                                PackedParams p) {
   const PackedTask tk = tasks[blockIdx.x];
   const PackedDev d = load_desc(tensors + tk.tensor);
+  const uint32_t t = sreg_i32(gld<uint32_t>(&p.adam.state->t)) + BEGINS;
+  const auto begin = [&](const PackedDev& d, const PackedParams& p) {
+    const uint32_t key = tensor_key(p.seed, t, d.tensor);
+    if constexpr (BEGINS) return StepScalars(d, p, adam_bias_short(t, p.adam.beta1, p.adam.beta2), key);
+    else return StepScalars(d, p, {p.adam.state->inv_bc1, p.adam.state->inv_sqrt_bc2}, key);
+  };
   bool bad;
   if constexpr (ROWS) {
-    bad = step_rows_chunk<F32, PRECISE>(d, p, tk.c0);
+    bad = step_rows_chunk<F32, PRECISE>(d, p, begin, tk.c0);
   } else {
     const int64_t left = d.n - tk.c0;
-    if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, tk.c0);
-    else bad = step_last_chunk<F32, PRECISE>(d, p, tk.c0, static_cast<uint32_t>(left));
+    if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, begin, tk.c0);
+    else bad = step_last_chunk<F32, PRECISE>(d, p, begin, tk.c0, static_cast<uint32_t>(left));
   }
   if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(p.adam.flags, 1u);
+  if constexpr (BEGINS) {
+    if (p.advance == nullptr) return;          // a launch after this one advances it
+    __syncthreads();                           // every wave has read the count
+    if (threadIdx.x == 0 && arrive_last(p.arrivals))
+      adam_store(p.advance, t, adam_bias_short(t, p.adam.beta1, p.adam.beta2));
+  }
 }
 
 // A chunk's plain values: first moments at `first`, second ones at `second`.
@@ -596,28 +603,37 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const PackedDev* __res
   }
 }
 
-}  // namespace
-
-namespace {
 template <bool F32, bool ROWS>
-const PackedTask* launch_step(bool precise, const PackedDev* tensors, const PackedTask* tasks, int n,
+const PackedTask* launch_step(bool precise, bool begins, const PackedDev* tensors, const PackedTask* tasks, int n,
                               const PackedParams& p, hipStream_t s) {
   if (n > 0) {
-    if (precise) adamw_packed_kernel<F32, true, ROWS><<<n, kThreads, 0, s>>>(tensors, tasks, p);
-    else adamw_packed_kernel<F32, false, ROWS><<<n, kThreads, 0, s>>>(tensors, tasks, p);
+    const auto kernel = precise ? (begins ? adamw_packed_kernel<F32, true, ROWS, true>
+                                          : adamw_packed_kernel<F32, true, ROWS, false>)
+                                : (begins ? adamw_packed_kernel<F32, false, ROWS, true>
+                                          : adamw_packed_kernel<F32, false, ROWS, false>);
+    kernel<<<n, kThreads, 0, s>>>(tensors, tasks, p);
   }
   return tasks + n;
 }
+
 }  // namespace
 
-hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, const int* n,
-                               const PackedParams& p, hipStream_t s) {
+hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, const int* n, bool begins,
+                               PackedParams p, hipStream_t s) {
   // a root below 2^-63 times at most 1 / sqrt(1 - b2) stays under half a unit (2^-24) of eps
   const bool precise = !(p.adam.eps * std::sqrt(1.f - p.adam.beta2) >= 0x1p-39f);
-  tasks = launch_step<false, false>(precise, tensors, tasks, n[0], p, s);
-  tasks = launch_step<false, true>(precise, tensors, tasks, n[1], p, s);
-  tasks = launch_step<true, false>(precise, tensors, tasks, n[2], p, s);
-  (void)launch_step<true, true>(precise, tensors, tasks, n[3], p, s);
+  int last = 0;
+  for (int k = 0; k < kPackKinds; ++k)
+    if (n[k] > 0) last = k;
+  AdamState* const state = const_cast<AdamState*>(p.adam.state);
+  const auto params = [&](int k) -> const PackedParams& {
+    p.advance = begins && k == last ? state : nullptr;
+    return p;
+  };
+  tasks = launch_step<false, false>(precise, begins, tensors, tasks, n[0], params(0), s);
+  tasks = launch_step<false, true>(precise, begins, tensors, tasks, n[1], params(1), s);
+  tasks = launch_step<true, false>(precise, begins, tensors, tasks, n[2], params(2), s);
+  (void)launch_step<true, true>(precise, begins, tensors, tasks, n[3], params(3), s);
   return hipGetLastError();
 }
 

@@ -274,3 +274,76 @@ __device__ __forceinline__ void update_w8_loaded(const UnitDev& u, int i, int j0
 }
 
 }  // namespace muon
+
+namespace muon {
+
+// Bias corrections of AdamW's step t.
+struct AdamBias { float inv_bc1, inv_sqrt_bc2; };
+__device__ __forceinline__ AdamBias adam_bias(uint32_t t, float beta1, float beta2) {
+  const double bc1 = 1.0 - pow(double(beta1), double(t));
+  const double bc2 = 1.0 - pow(double(beta2), double(t));
+  return {float(1.0 / bc1), float(1.0 / sqrt(bc2))};
+}
+
+// The same by repeated squaring, for kernels in which every wave takes them:
+// some 20 dependent products instead of two calls of pow (which took 1.2 us of
+// a launch of 6.6 us).  Each power is off by t units of 2^-53, so its float32 result is the
+// same but where the exact one lies that close to a rounding border.
+__device__ __forceinline__ AdamBias adam_bias_short(uint32_t t, float beta1, float beta2) {
+  double p1 = 1.0, p2 = 1.0, b1 = beta1, b2 = beta2;
+  for (; t; t >>= 1) {
+    if (t & 1) {
+      p1 *= b1;
+      p2 *= b2;
+    }
+    b1 *= b1;
+    b2 *= b2;
+  }
+  return {float(1.0 / (1.0 - p1)), float(1.0 / sqrt(1.0 - p2))};
+}
+
+// Next step of the AdamW count: t and the bias corrections of that step.
+__device__ __forceinline__ void adam_store(AdamState* st, uint32_t t, const AdamBias& b) {
+  st->t = t;
+  st->inv_bc1 = b.inv_bc1;
+  st->inv_sqrt_bc2 = b.inv_sqrt_bc2;
+}
+__device__ __forceinline__ void adam_advance(AdamState* st, float beta1, float beta2) {
+  const uint32_t t = st->t + 1;
+  adam_store(st, t, adam_bias(t, beta1, beta2));
+}
+
+// Called by one thread of every block of a launch: true in the one that comes
+// last.  Counts at one address take about 10 ns each, so the blocks count in
+// kArriveGroups groups and the last of each group at the root.  The counters
+// are zero again afterwards.  What a block has stored past its die's caches
+// (device-scope atomic stores) and waited for before it arrives, the last
+// block reads with device-scope atomic loads; nothing else passes between
+// blocks, so no cache is written back or invalidated.
+__device__ __forceinline__ bool arrive_last(Arrivals* a) {
+  const uint32_t g = blockIdx.x % kArriveGroups;
+  const uint32_t members = (gridDim.x - g + kArriveGroups - 1) / kArriveGroups;
+  const uint32_t groups = gridDim.x < kArriveGroups ? gridDim.x : kArriveGroups;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if (__hip_atomic_fetch_add(&a->group[g].n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != members - 1) return false;
+  a->group[g].n = 0;
+  if (__hip_atomic_fetch_add(&a->root.n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1) return false;
+  a->root.n = 0;
+  return true;
+}
+
+// Random words of the packed moments' rounding (adamw_packed.hip): two rounds
+// of xor-shift and multiplication, a bijection of 32 bits, and the key of one
+// tensor at step t.
+constexpr uint32_t kGolden = 0x9E3779B9u;     // 2^32 over the golden ratio, odd
+constexpr uint32_t kRoot3 = 0xBB67AE85u;      // 2^32 (sqrt(3) - 1), odd
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x = (x ^ (x >> 16)) * kGolden;
+  x = (x ^ (x >> 15)) * kRoot3;
+  return x ^ (x >> 16);
+}
+__device__ __forceinline__ uint32_t tensor_key(const RoundingSeed& seed, uint32_t t, uint32_t tensor) {
+  return mix(mix(mix(mix(seed.lo) + seed.hi) + t) + tensor);
+}
+
+}  // namespace muon

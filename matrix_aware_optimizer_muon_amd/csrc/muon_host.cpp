@@ -2,9 +2,10 @@
 // tile lists, workspace carve-up), descriptor upload and kernel sequencing.
 //
 // Plan of one step:
-//   grad norm (2 launches, only with a maximum set: sums, norm and factor)
-//   adamw     (only with kind-ADAMW tensors: count tick, update of the tensors
-//             with float32 moments, update of those with 8-bit ones)
+//   grad norm (1 launch, only with a maximum set; then it also does the
+//             AdamW count)
+//   adamw     (only with kind-ADAMW tensors: count, update of the tensors with
+//             float32 moments, update of those with 8-bit ones)
 //             Muon README "Usage"
 // then per NS-precision group, all matrices of the group at once:
 //   momentum  (1 launch)      Muon README "Hyperparameter tuning"
@@ -145,12 +146,14 @@ struct Plan {
   std::vector<int64_t> packed_value0;  // elements of the packed tensors before each
   std::vector<PackedTask> packed_tasks;
   int packed_kind[kPackKinds] = {};  // packed tasks of each kind of tensor (launch_adamw_packed)
+  bool packed_begins = false;        // few packed tensors alone: their launch advances the AdamW count itself
   int64_t packed_elems = 0;
   size_t off_packed_dev = 0, off_packed_tasks = 0;
+  size_t off_arrivals = 0;
   std::vector<int64_t> norm_chunk0;  // per tensor: gradient-norm chunks of the tensors before it
   int64_t norm_chunks = 0;
   bool with_norm = false;            // the workspace holds the gradient norm's table and sums
-  size_t off_norm_dev = 0, off_norm_part = 0, off_norm_state = 0;
+  size_t off_norm_dev = 0, off_norm_first = 0, off_norm_part = 0, off_norm_state = 0;
   size_t off_flags = 0, off_partials = 0, off_norms = 0;
   size_t off_mpart = 0;              // refresh scratch (moment partials, float64 S^-1 sum), all slots
   size_t meta_bytes = 0, total = 0;
@@ -501,6 +504,8 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
     plan.packed_kind[k] = int(packed_by_kind[k].size());
     plan.packed_tasks.insert(plan.packed_tasks.end(), packed_by_kind[k].begin(), packed_by_kind[k].end());
   }
+  plan.packed_begins = plan.adam_tasks.empty() && !plan.packed_tasks.empty() &&
+                       plan.packed_tasks.size() <= size_t(kPackBeginMost);
   plan.with_norm = with_norm;
   for (int32_t i = 0; i < n; ++i) {
     plan.norm_chunk0.push_back(plan.norm_chunks);
@@ -638,9 +643,13 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   plan.off_adam_state = off; off = align_up(off + sizeof(AdamState));
   plan.off_packed_dev = off; off = align_up(off + sizeof(PackedDev) * plan.packed_tensors.size());
   plan.off_packed_tasks = off; off = align_up(off + sizeof(PackedTask) * plan.packed_tasks.size());
+  if (plan.with_norm || !plan.packed_tensors.empty()) {
+    plan.off_arrivals = off; off = align_up(off + sizeof(Arrivals));
+  }
   if (plan.with_norm) {
     plan.off_norm_dev = off; off = align_up(off + sizeof(NormDev) * size_t(n));
-    plan.off_norm_part = off; off = align_up(off + sizeof(double) * size_t(std::min<int64_t>(plan.norm_chunks, kNormBlocks)));
+    plan.off_norm_first = off; off = align_up(off + sizeof(int32_t) * size_t(norm_blocks(plan.norm_chunks)));
+    plan.off_norm_part = off; off = align_up(off + sizeof(double) * size_t(norm_blocks(plan.norm_chunks)));
     plan.off_norm_state = off; off = align_up(off + sizeof(NormState));
   }
   plan.meta_bytes = off;
@@ -780,7 +789,6 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
   }
   if (!plan.adam_tasks.empty())
     std::memcpy(meta.data() + plan.off_adam_tasks, plan.adam_tasks.data(), plan.adam_tasks.size() * sizeof(AdamTask));
-  auto al16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   for (size_t pi = 0; pi < plan.packed_tensors.size(); ++pi) {
     const muon_tensor_t& t = ts[plan.packed_tensors[pi]];
     PackedDev d;
@@ -808,7 +816,6 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
                 plan.packed_tasks.size() * sizeof(PackedTask));
   for (size_t i = 0; plan.with_norm && i < plan.norm_chunk0.size(); ++i) {
     const muon_tensor_t& t = ts[i];
-    const int64_t es = t.dtype == MUON_F32 ? 4 : 2;
     NormDev d;
     std::memset(&d, 0, sizeof(d));
     d.grad = t.grad;
@@ -818,8 +825,15 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.chunk0 = plan.norm_chunk0[i];
     d.f32 = t.dtype == MUON_F32;
     d.flat = t.rows == 1 || t.ld_grad == t.cols;
-    d.vec = al16(t.grad) && (d.flat || (t.cols % 8 == 0 && (t.ld_grad * es) % 16 == 0));
+    d.vec = d.flat || t.cols % 8 == 0;
     std::memcpy(meta.data() + plan.off_norm_dev + i * sizeof(NormDev), &d, sizeof(d));
+  }
+  const int nb = plan.with_norm ? norm_blocks(plan.norm_chunks) : 0;
+  for (int b = 0; b < nb; ++b) {              // the last tensor whose first chunk is not after the block's
+    const auto it = std::upper_bound(plan.norm_chunk0.begin(), plan.norm_chunk0.end(),
+                                     norm_first_chunk(plan.norm_chunks, b, nb));
+    const int32_t first = int32_t(it - plan.norm_chunk0.begin()) - 1;
+    std::memcpy(meta.data() + plan.off_norm_first + size_t(b) * sizeof(int32_t), &first, sizeof(first));
   }
   return meta;
 }
@@ -862,15 +876,21 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
   };
   Range step_range("muon.step");
   if (!mark()) return fail(MUON_ERR_HIP, "hipEventRecord failed");
-  // before the fork: every gradient's reader multiplies by the factor
+  // before the fork: every gradient's reader multiplies by the factor.  With
+  // a norm to take, its launch also advances the AdamW count.
   const float* factor = nullptr;
-  if (h->max_norm > 0.f) {
+  const bool with_norm = h->max_norm > 0.f;
+  Arrivals* arrivals = reinterpret_cast<Arrivals*>(h->ws + plan.off_arrivals);
+  AdamState* const adam_state = reinterpret_cast<AdamState*>(h->ws + plan.off_adam_state);
+  if (with_norm) {
     Range r("muon.grad_norm");
     NormState* ns = reinterpret_cast<NormState*>(h->ws + plan.off_norm_state);
-    hipError_t e = launch_grad_norm(reinterpret_cast<const NormDev*>(h->ws + plan.off_norm_dev),
-                                    int(h->tensors.size()), plan.norm_chunks,
-                                    reinterpret_cast<double*>(h->ws + plan.off_norm_part), ns, h->max_norm,
-                                    h->norm_out, s);
+    const NormParams np{reinterpret_cast<const NormDev*>(h->ws + plan.off_norm_dev),
+                        reinterpret_cast<const int32_t*>(h->ws + plan.off_norm_first), plan.norm_chunks,
+                        int32_t(h->tensors.size()), h->max_norm,
+                        reinterpret_cast<double*>(h->ws + plan.off_norm_part), ns, arrivals, h->norm_out,
+                        plan.has_adam() ? adam_state : nullptr, hp.adam_beta1, hp.adam_beta2};
+    const hipError_t e = launch_grad_norm(np, s);
     if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("grad norm launch: ") + hipGetErrorString(e));
     factor = &ns->factor;
   }
@@ -896,8 +916,9 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
   }
   auto launch_adam = [&](hipStream_t as) -> muon_status_t {
     Range r("muon.adamw");
-    AdamState* st = reinterpret_cast<AdamState*>(h->ws + plan.off_adam_state);
-    hipError_t e = launch_adam_tick(st, hp.adam_beta1, hp.adam_beta2, as);
+    AdamState* st = adam_state;
+    const bool packed_begins = plan.packed_begins && !with_norm;
+    hipError_t e = with_norm || packed_begins ? hipSuccess : launch_adam_tick(st, hp.adam_beta1, hp.adam_beta2, as);
     AdamParams ap{hp.adam_lr, hp.adam_beta1, hp.adam_beta2, hp.adam_eps, hp.adam_weight_decay, st,
                   reinterpret_cast<uint32_t*>(h->ws + plan.off_flags), factor};
     if (e == hipSuccess)
@@ -907,8 +928,9 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     if (e == hipSuccess && !plan.packed_tasks.empty())
       e = launch_adamw_packed(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
                               reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
-                              plan.packed_kind,
-                              PackedParams{ap, uint32_t(h->rounding_seed), uint32_t(h->rounding_seed >> 32)}, as);
+                              plan.packed_kind, packed_begins,
+                              PackedParams{ap, nullptr, arrivals,
+                                           {uint32_t(h->rounding_seed), uint32_t(h->rounding_seed >> 32)}}, as);
     if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("adamw launch: ") + hipGetErrorString(e));
     return MUON_OK;
   };
@@ -1048,11 +1070,13 @@ std::string plan_json(const Plan& plan, const muon_hparams_t& hp) {
     first = false;
   }
   if (plan.has_adam()) {
-    if (!first) s += ",";
-    s += "\"adam_tick\"";
-    if (!plan.adam_tasks.empty()) s += ",\"adamw\"";
-    if (!plan.packed_tasks.empty()) s += ",\"adamw_packed\"";
-    first = false;
+    const char* const launches[] = {plan.packed_begins ? "" : "adam_tick", plan.adam_tasks.empty() ? "" : "adamw",
+                                    plan.packed_tasks.empty() ? "" : "adamw_packed"};
+    for (const char* name : launches) {
+      if (!*name) continue;
+      s += std::string(first ? "\"" : ",\"") + name + "\"";
+      first = false;
+    }
   }
   for (const Group& g : plan.groups) {
     if (g.units.empty()) continue;
