@@ -47,7 +47,7 @@ constexpr int kThreads = 256;
 // A thread takes 8 elements in groups of 16 bytes of the tensor (8 of bf16, 4
 // of float32), so that a wave's access is one run of 1 KB: at half that, 32
 // bytes apart, float32 values were written back in parts (unpacking 38.6 M
-// elements 113 us with streaming stores, 67 us without, XX as it is now).
+// elements 113 us with streaming stores, 67 us without, 64 us as it is now).
 constexpr int kPer = 8;
 constexpr int kWave = 64 * kPer;              // elements per wave
 static_assert(kThreads * kPer == kPackChunk && kWave == 2 * kPackBlock, "a wave holds two blocks");
@@ -77,8 +77,10 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
   return x;
 }
 
-// Streaming accesses: no buffer here is read again before the caches have
-// turned over.
+// Streaming accesses for weights, gradients, values and every store: of 82 M
+// bf16 elements a step and its unpacking took 155 + 83 us without them, 145 +
+// 73 with them.  The moments' bytes are read the ordinary way: read streaming
+// they took unpacking from 71 to 80 us and a float32 step from 93 to 100.
 template <typename T>
 __device__ __forceinline__ T gld_nt(const void* p) {
   return __builtin_nontemporal_load((const MUON_GLOBAL T*)p);
@@ -465,9 +467,15 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
   return bad;
 }
 
-// Tensors with gaps between their rows (ROWS) have a kernel of their own: the
-// other one then needs 64 registers, not 78, for 8 waves a SIMD instead of 6
-// (82 M bf16 elements 128 against 137 us).
+// Tensors with gaps between their rows (ROWS) have a kernel of their own, as
+// their addressing took the other one from 64 to 78 registers, from 8 waves a
+// SIMD to 6 (82 M bf16 elements 128 and 137 us).
+//
+// HBM-bound: 10 bytes per bf16 element, 16 per float32 one: 82 M bf16 elements
+// in 128 us (6.4 TB/s), 38.6 M float32 ones in 93 us (6.6 TB/s).  The vector
+// units are busy for about 100 of the 128 us (45 instructions an element), so
+// the root and the reciprocal are the hardware's: with the language's, 65
+// instructions an element, the same took 151 us, all of them.
 // BEGINS: no launch has advanced the step count before this one.  Every wave
 // takes the next step's bias corrections itself, while its loads are under
 // way, and the last block advances the count (launch_adamw_packed).

@@ -152,8 +152,9 @@ struct Plan {
   size_t off_arrivals = 0;
   std::vector<int64_t> norm_chunk0;  // per tensor: gradient-norm chunks of the tensors before it
   int64_t norm_chunks = 0;
+  std::vector<int32_t> chunk_tensor; // per gradient-norm chunk: its tensor
   bool with_norm = false;            // the workspace holds the gradient norm's table and sums
-  size_t off_norm_dev = 0, off_norm_first = 0, off_norm_part = 0, off_norm_state = 0;
+  size_t off_norm_dev = 0, off_chunk_tensor = 0, off_norm_part = 0, off_norm_state = 0;
   size_t off_flags = 0, off_partials = 0, off_norms = 0;
   size_t off_mpart = 0;              // refresh scratch (moment partials, float64 S^-1 sum), all slots
   size_t meta_bytes = 0, total = 0;
@@ -510,6 +511,7 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   for (int32_t i = 0; i < n; ++i) {
     plan.norm_chunk0.push_back(plan.norm_chunks);
     plan.norm_chunks += (ts[i].rows * ts[i].cols + kNormChunk - 1) / kNormChunk;
+    if (with_norm) plan.chunk_tensor.resize(size_t(plan.norm_chunks), i);
   }
   // units
   for (int32_t i = 0; i < n; ++i) {
@@ -648,7 +650,7 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   }
   if (plan.with_norm) {
     plan.off_norm_dev = off; off = align_up(off + sizeof(NormDev) * size_t(n));
-    plan.off_norm_first = off; off = align_up(off + sizeof(int32_t) * size_t(norm_blocks(plan.norm_chunks)));
+    plan.off_chunk_tensor = off; off = align_up(off + sizeof(int32_t) * plan.chunk_tensor.size());
     plan.off_norm_part = off; off = align_up(off + sizeof(double) * size_t(norm_blocks(plan.norm_chunks)));
     plan.off_norm_state = off; off = align_up(off + sizeof(NormState));
   }
@@ -828,13 +830,9 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.vec = d.flat || t.cols % 8 == 0;
     std::memcpy(meta.data() + plan.off_norm_dev + i * sizeof(NormDev), &d, sizeof(d));
   }
-  const int nb = plan.with_norm ? norm_blocks(plan.norm_chunks) : 0;
-  for (int b = 0; b < nb; ++b) {              // the last tensor whose first chunk is not after the block's
-    const auto it = std::upper_bound(plan.norm_chunk0.begin(), plan.norm_chunk0.end(),
-                                     norm_first_chunk(plan.norm_chunks, b, nb));
-    const int32_t first = int32_t(it - plan.norm_chunk0.begin()) - 1;
-    std::memcpy(meta.data() + plan.off_norm_first + size_t(b) * sizeof(int32_t), &first, sizeof(first));
-  }
+  if (plan.with_norm && !plan.chunk_tensor.empty())
+    std::memcpy(meta.data() + plan.off_chunk_tensor, plan.chunk_tensor.data(),
+                plan.chunk_tensor.size() * sizeof(int32_t));
   return meta;
 }
 
@@ -886,8 +884,8 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     Range r("muon.grad_norm");
     NormState* ns = reinterpret_cast<NormState*>(h->ws + plan.off_norm_state);
     const NormParams np{reinterpret_cast<const NormDev*>(h->ws + plan.off_norm_dev),
-                        reinterpret_cast<const int32_t*>(h->ws + plan.off_norm_first), plan.norm_chunks,
-                        int32_t(h->tensors.size()), h->max_norm,
+                        reinterpret_cast<const int32_t*>(h->ws + plan.off_chunk_tensor), plan.norm_chunks,
+                        h->max_norm,
                         reinterpret_cast<double*>(h->ws + plan.off_norm_part), ns, arrivals, h->norm_out,
                         plan.has_adam() ? adam_state : nullptr, hp.adam_beta1, hp.adam_beta2};
     const hipError_t e = launch_grad_norm(np, s);

@@ -225,13 +225,11 @@ struct PackedParams {
 };
 
 // Global gradient norm: every registered gradient as a run of n elements cut
-// in chunks of kNormChunk, the chunks of all tensors numbered through; each
-// block sums a contiguous range of them.
+// in chunks of kNormChunk, the chunks of all tensors numbered through; block b
+// of n sums chunks b, b + n and so on.
 constexpr int kNormChunk = 8192;       // 256 threads x 32 elements
-constexpr int kNormBlocks = 2048;      // most blocks (and partial sums)
+constexpr int kNormBlocks = 1024;      // most blocks (and partial sums): four waves a SIMD
 inline int norm_blocks(int64_t chunks) { return static_cast<int>(chunks < kNormBlocks ? chunks : kNormBlocks); }
-// First chunk of block b of `blocks`.
-__host__ __device__ inline int64_t norm_first_chunk(int64_t chunks, int b, int blocks) { return chunks * b / blocks; }
 struct NormDev {
   const void* grad;
   int64_t ld, n, cols;                 // cols: row length, of use only where flat is 0
@@ -241,9 +239,8 @@ struct NormDev {
 struct NormState { float norm, factor; };   // of the latest step, in the workspace
 struct NormParams {
   const NormDev* tensors;
-  const int32_t* first;                // tensor of each block's first chunk
+  const int32_t* chunk_tensor;         // tensor of each chunk
   int64_t chunks;
-  int32_t n_tensors;
   float max_norm;
   double* partials;                    // one sum per block
   NormState* state;
