@@ -184,8 +184,9 @@ muon_status_t muon_init(muon_handle_t* out, const muon_tensor_t* tensors, int32_
  * 64 MiB per GPU (held by each GPU the library runs on until the process
  * ends), so the call takes no workspace and allocates nothing on the device.
  * The handle creates no streams or events either: muon_step runs every launch
- * on the caller's stream.  Requests whose workspace (muon_workspace_size)
- * exceeds 64 MiB return MUON_ERR_WORKSPACE_TOO_SMALL before any GPU call.
+ * on the caller's stream.  Requests whose workspace (muon_workspace_size, less
+ * the sums of muon_set_max_grad_norm where those alone do not fit) exceeds 64
+ * MiB return MUON_ERR_WORKSPACE_TOO_SMALL before any GPU call.
  * The array belongs to the calling thread's current device.  All static
  * handles of one GPU share it: each muon_init_static zero-fills it for its
  * own plan, which supersedes every earlier static handle of that GPU (their
@@ -277,10 +278,11 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * value itself: rounded to nearest, a moment whose change is less than half
  * the distance of two values would stay where it is.  The random bits are a
  * function of (seed, step count, place of the tensor in the list, element), so
- * equal runs give equal bytes, also from a replayed graph.  The noise this adds
- * to a moment is about 0.04 / sqrt(1 - beta^2) of it: 8 % of the first moment at
- * beta1 = 0.9, 12 % of the second at beta2 = 0.95 (6 % of its root), but 26 % at
- * beta2 = 0.99 and over 80 % at 0.999: take float32 moments there.
+ * equal runs give equal bytes, also from a replayed graph.  Against float32
+ * moments of the same independent normal gradients the second moment is then
+ * off by 13, 18 and 21 % (rms, mean zero) at beta2 = 0.95, 0.99 and 0.999, the
+ * first at beta1 = 0.9 by 8 % of its rms, and m / sqrt(v) by 10 to 13 % of its
+ * own.
  * A first moment that is not finite stays so (NaN) and sets flag bit 0; the
  * other elements of its block are not affected.
  *
@@ -314,8 +316,9 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
  * norm_out: NULL, or device memory for two floats that each step fills with
  * (norm, factor) on its stream; it must live as long as it is set.  Host only;
  * a captured step keeps what was set when it was captured.  A handle of
- * muon_init_static whose request fills the static scratch up to the last few
- * kilobytes returns MUON_ERR_WORKSPACE_TOO_SMALL. */
+ * muon_init_static whose request fits the static scratch only without the
+ * norm's sums (some kilobytes, and 4 bytes per 8192 elements) returns
+ * MUON_ERR_WORKSPACE_TOO_SMALL for max_norm > 0. */
 muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* norm_out);
 
 /* Synchronises `stream` and returns the sticky flag word:

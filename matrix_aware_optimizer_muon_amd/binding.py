@@ -294,6 +294,7 @@ def _packed_adam_desc(param, grad, exp_avg, exp_avg_sq, lr_mult) -> MuonTensor:
     d.dtype, d.split_rows, d.precond, d.lr_mult = dt, 0, -1, lr_mult
     d.kind, d.state_bits = KIND_ADAMW, 8
     d.update_out = None
+    d.torch_device = param.device        # MuonStep refuses one that is not its own
     return d
 
 
@@ -348,6 +349,7 @@ class MuonStep:
         library to run this handle on (e.g. the bounds-checking debug build,
         build.DEBUG_LIB); default the one load_library() returns."""
         torch = _torch()
+        descs = list(descs)
         self._lib = load_library(library)
         self.hp = hp if hp is not None else default_hparams()
         self._descs, self._n = _array(list(descs), MuonTensor)
@@ -356,6 +358,9 @@ class MuonStep:
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        for d in descs:
+            if getattr(d, "torch_device", self.device) != self.device:
+                raise ValueError(f"a tensor on {d.torch_device} in a handle on {self.device}")
         self._keep = list(keepalive)
         self._packed_elements = sum(d.rows * d.cols for d in self._descs[:self._n]
                                     if d.kind == KIND_ADAMW and d.state_bits == 8)

@@ -133,6 +133,34 @@ def test_a_vanished_gradient_decays_only_with_random_rounding():
     assert abs(rand.mean() / (1.125 * 0.95 ** steps) - 1) < 6 * 0.041 / np.sqrt(1 - 0.95 ** 2) / np.sqrt(n / 16)
 
 
+@pytest.mark.parametrize("beta2,second", [(0.95, 0.13), (0.99, 0.18), (0.999, 0.21)])
+def test_stated_noise_against_float_moments(beta2, second):
+    # include/muon.h: the second moment off by `second` (rms), the first by 8 % of its rms, m / sqrt(v) by 10 to
+    # 13 % of its own, each to the digits given there.  The second moment's noise builds up with its own time
+    # constant: after t steps its variance is 1 - beta2^(2 t) of what it comes to.
+    n, b1, f = 8192, 0.9, np.float32
+    rng = np.random.default_rng(0)
+    s = 2.0 ** rng.uniform(-4, 0, n)
+    m, v, me, ve = np.zeros(n), s ** 2, np.zeros(n), s ** 2
+    steps = int(min(2000, 5 / (1 - beta2)))
+    dm, dv, du, ue, share = [], [], [], [], []
+    for t in range(steps):
+        g = s * rng.normal(0, 1, n)
+        m1, v1 = pm.moments_f32(g, m, v, (b1, beta2))
+        me, ve = b1 * me + (1 - b1) * g, beta2 * ve + (1 - beta2) * g * g
+        m, v = pm.decode(*pm.encode(m1, v1, pm.words(1, t, 0, n)), n)
+        if t > steps // 2 and t % max(1, steps // 40) == 0:
+            dv.append(v1 / ve - 1)
+            dm.append((m1 - me) / s)
+            du.append(m1 / np.sqrt(v1.astype(np.float64)) - me / np.sqrt(ve))
+            ue.append(me / np.sqrt(ve))
+            share.append(1 - beta2 ** (2 * t))
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    assert abs(rms(dv) - second * np.sqrt(np.mean(share))) < 0.01 and abs(np.mean(dv)) < 0.01
+    assert abs(rms(dm) / np.sqrt((1 - b1) / (1 + b1)) - 0.08) < 0.01
+    assert 0.09 < rms(du) / rms(ue) < 0.14
+
+
 def test_planted_mistakes_show():
     n = 512
     rng = _rng(6)
