@@ -326,9 +326,9 @@ __device__ __forceinline__ bool arrive_last(Arrivals* a) {
   const uint32_t groups = gridDim.x < kArriveGroups ? gridDim.x : kArriveGroups;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   if (__hip_atomic_fetch_add(&a->group[g].n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != members - 1) return false;
-  a->group[g].n = 0;
+  __hip_atomic_store(&a->group[g].n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (__hip_atomic_fetch_add(&a->root.n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != groups - 1) return false;
-  a->root.n = 0;
+  __hip_atomic_store(&a->root.n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return true;
 }
 

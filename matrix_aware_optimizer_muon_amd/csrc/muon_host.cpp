@@ -56,6 +56,8 @@ muon_status_t guarded(F&& body) {
   try {
     return body();
   } catch (const std::exception&) {
+    g_last_error.clear();
+    g_last_error += "out of memory";   // short enough to need none
     return MUON_ERR_UNSUPPORTED;
   }
 }
@@ -1125,28 +1127,32 @@ void muon_default_hparams(muon_hparams_t* hp) {
 
 muon_status_t muon_workspace_size(const muon_tensor_t* tensors, int32_t n_tensors, const muon_precond_t* preconds,
                                   int32_t n_preconds, const muon_hparams_t* hp, size_t* bytes) {
-  if (!bytes) return fail(MUON_ERR_NULL_ARG, "bytes is NULL");
-  Plan plan;
-  muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
-  if (st != MUON_OK) return st;
-  *bytes = plan.total;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!bytes) return fail(MUON_ERR_NULL_ARG, "bytes is NULL");
+    Plan plan;
+    muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
+    if (st != MUON_OK) return st;
+    *bytes = plan.total;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_plan_describe(const muon_tensor_t* tensors, int32_t n_tensors, const muon_precond_t* preconds,
                                  int32_t n_preconds, const muon_hparams_t* hp, char* buf, size_t len,
                                  size_t* needed) {
-  Plan plan;
-  muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
-  if (st != MUON_OK) return st;
-  const std::string js = plan_json(plan, *hp);
-  if (needed) *needed = js.size() + 1;
-  if (buf && len) {
-    const size_t k = std::min(len - 1, js.size());
-    std::memcpy(buf, js.data(), k);
-    buf[k] = 0;
-  }
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    Plan plan;
+    muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
+    if (st != MUON_OK) return st;
+    const std::string js = plan_json(plan, *hp);
+    if (needed) *needed = js.size() + 1;
+    if (buf && len) {
+      const size_t k = std::min(len - 1, js.size());
+      std::memcpy(buf, js.data(), k);
+      buf[k] = 0;
+    }
+    return MUON_OK;
+  });
 }
 
 }  // extern "C"
@@ -1280,47 +1286,51 @@ extern "C" {
 muon_status_t muon_init(muon_handle_t* out, const muon_tensor_t* tensors, int32_t n_tensors,
                         const muon_precond_t* preconds, int32_t n_preconds, const muon_hparams_t* hp,
                         void* workspace, size_t workspace_bytes, void* stream) {
-  if (!out) return fail(MUON_ERR_NULL_ARG, "out is NULL");
-  *out = nullptr;
-  Plan plan;
-  muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
-  if (st != MUON_OK) return st;
-  if (!workspace) return fail(MUON_ERR_NULL_ARG, "workspace is NULL");
-  if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
-    return fail(MUON_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-  if (workspace_bytes < plan.total)
-    return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
-                "workspace has " + std::to_string(workspace_bytes) + " bytes, needs " + std::to_string(plan.total));
-  return init_handle(out, std::move(plan), tensors, n_tensors, hp, workspace, stream, true);
+  return guarded([&]() -> muon_status_t {
+    if (!out) return fail(MUON_ERR_NULL_ARG, "out is NULL");
+    *out = nullptr;
+    Plan plan;
+    muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan);
+    if (st != MUON_OK) return st;
+    if (!workspace) return fail(MUON_ERR_NULL_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % kAlign)
+      return fail(MUON_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    if (workspace_bytes < plan.total)
+      return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
+                  "workspace has " + std::to_string(workspace_bytes) + " bytes, needs " + std::to_string(plan.total));
+    return init_handle(out, std::move(plan), tensors, n_tensors, hp, workspace, stream, true);
+  });
 }
 
 muon_status_t muon_init_static(muon_handle_t* out, const muon_tensor_t* tensors, int32_t n_tensors,
                                const muon_precond_t* preconds, int32_t n_preconds, const muon_hparams_t* hp,
                                void* stream) {
-  if (!out) return fail(MUON_ERR_NULL_ARG, "out is NULL");
-  *out = nullptr;
-  Plan plan;
-  muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true);
-  if (st == MUON_OK && plan.total > kStaticScratchBytes)   // the gradient norm's table may be what does not fit
-    st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true, /*with_norm=*/false);
-  if (st != MUON_OK) return st;
-  if (plan.total > kStaticScratchBytes)
-    return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
-                "the request needs " + std::to_string(plan.total) + " bytes of workspace; the static scratch holds " +
-                    std::to_string(kStaticScratchBytes) + " (use muon_init with a caller workspace)");
-  int dev = -1;
-  void* ptr = nullptr;
-  if ((st = static_scratch(&dev, &ptr)) != MUON_OK) return st;
-  uint64_t gen;
-  {
-    std::lock_guard<std::mutex> lk(g_static_mu);
-    gen = ++g_static_gen[dev];
-  }
-  st = init_handle(out, std::move(plan), tensors, n_tensors, hp, ptr, stream, false);
-  if (st != MUON_OK) return st;
-  (*out)->static_device = dev;
-  (*out)->static_generation = gen;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!out) return fail(MUON_ERR_NULL_ARG, "out is NULL");
+    *out = nullptr;
+    Plan plan;
+    muon_status_t st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true);
+    if (st == MUON_OK && plan.total > kStaticScratchBytes)   // the gradient norm's table may be what does not fit
+      st = build_plan(tensors, n_tensors, preconds, n_preconds, hp, plan, /*single_lane=*/true, /*with_norm=*/false);
+    if (st != MUON_OK) return st;
+    if (plan.total > kStaticScratchBytes)
+      return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
+                  "the request needs " + std::to_string(plan.total) + " bytes of workspace; the static scratch holds " +
+                      std::to_string(kStaticScratchBytes) + " (use muon_init with a caller workspace)");
+    int dev = -1;
+    void* ptr = nullptr;
+    if ((st = static_scratch(&dev, &ptr)) != MUON_OK) return st;
+    uint64_t gen;
+    {
+      std::lock_guard<std::mutex> lk(g_static_mu);
+      gen = ++g_static_gen[dev];
+    }
+    st = init_handle(out, std::move(plan), tensors, n_tensors, hp, ptr, stream, false);
+    if (st != MUON_OK) return st;
+    (*out)->static_device = dev;
+    (*out)->static_generation = gen;
+    return MUON_OK;
+  });
 }
 
 namespace {

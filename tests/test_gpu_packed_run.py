@@ -222,3 +222,57 @@ def test_tensors_of_another_device_are_refused():
     p = torch.zeros(100)
     with pytest.raises(ValueError):
         mm.MuonStep([mm.adam_tensor_desc(p, p.clone(), mm.packed_moment(p), mm.packed_moment(p))])
+
+
+def test_clipping_before_the_preconditioner():
+    say("case: clipped Newton-Muon step against one on gradients scaled beforehand")
+    hp = mm.default_hparams()
+    pc = mm.MuonPrecond()
+    pc.d, pc.nblocks = 128, 1
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    acts = torch.randn(2048, 128, device="cuda", generator=gen)
+    w = torch.randn(256, 128, device="cuda", generator=gen) * 0.02
+    g = torch.randn(256, 128, device="cuda", generator=gen) * 1e-2
+    out = []
+    factor = None
+    for clipped in (True, False):
+        p, gg, m = w.clone(), g.clone(), torch.zeros_like(w)
+        if not clipped:
+            gg *= factor
+        st = mm.MuonStep([mm.tensor_desc(p, gg, m, precond=0)], hp, [pc], keepalive=[p, gg, m])
+        st.precond_refresh(0, 0, acts)
+        if clipped:
+            st.set_max_grad_norm(0.25)
+        st.step()
+        if clipped:
+            factor = st.grad_norm[1].clone()
+            assert 0 < factor.item() < 1
+        out.append((m.cpu().numpy(), p.cpu().numpy()))
+        assert st.flags() == 0
+        st.close()
+    # (f G) S^-1 and f (G S^-1): float32 sums of 128 products of either, each rounded 128 times at most
+    assert rel_f(out[0][0], out[1][0]) <= 128 * 2.0 ** -24
+    # float32 Newton-Schulz of two momenta that close: its own parity bar, 1e-5, on the update lr * O; the
+    # weights are larger than the update
+    assert rel_f(out[0][1], out[1][1]) <= 1e-5
+
+
+def test_debug_build_matches():
+    say("case: the bounds-checking build, packed and clipped, bitwise as the release build")
+    from matrix_aware_optimizer_muon_amd import build as BLD
+    hp = mm.default_hparams()
+    states = []
+    for library in (None, BLD.DEBUG_LIB):
+        xs = [Packed((420, k), s, d) for k, (s, d) in enumerate([((300, 64), "bf16"), ((5001,), "f32")])]
+        st = mm.MuonStep([x.desc() for x in xs], hp, library=library)
+        for t in (1, 2, 3):
+            if t == 2:
+                st.set_max_grad_norm(0.25)
+            for x in xs:
+                x.grad(t)
+            st.step()
+        states.append([y.clone() for x in xs for y in (x.dW, x.dM, x.dV)] + [st.grad_norm.clone(), st.unpack_moments()])
+        assert st.flags() == 0
+        st.close()
+    for a, b in zip(*states):
+        assert torch.equal(a, b)
