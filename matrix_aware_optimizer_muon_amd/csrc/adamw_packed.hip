@@ -422,8 +422,8 @@ struct Place {
   }
 };
 
-// A chunk of a tensor with gaps between its rows: group by group where rows
-// hold whole groups, else one element after another.
+// A chunk of a tensor with gaps between its rows: whole groups inside a row,
+// one element after another where a row ends in a group.
 template <bool F32, bool PRECISE, typename Begin>
 __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const PackedParams& p, const Begin& begin,
                                                  int64_t c0) {
@@ -438,7 +438,7 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
     pk.load(d, i);
     float w[W], g[W];
     const Place pl(d, i);
-    const bool whole = d.vec && i + W <= d.n;
+    const bool whole = pl.c + W <= d.cols && i + W <= d.n;
     if (whole) {
       Raw<F32> wr, gr;
       wr.load(d.param, pl.at(d.ld_param));

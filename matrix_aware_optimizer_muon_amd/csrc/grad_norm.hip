@@ -85,7 +85,7 @@ __device__ __forceinline__ void add_any_chunk(const NormDev& d, int64_t c0, doub
       r = i / d.cols;
       col = i - r * d.cols;
     }
-    if (d.vec && i + W <= end) {
+    if ((d.flat || col + W <= d.cols) && i + W <= end) {
       add_squares<F32>(gld<u32x4h_t>(base + (r * d.ld + col) * es), s);
       continue;
     }

@@ -810,7 +810,6 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.v_scales = reinterpret_cast<uint16_t*>(d.v + d.blocks * kPackBlock);
     d.value0 = plan.packed_value0[pi];
     d.f32 = t.dtype == MUON_F32;
-    d.vec = gapless(t) || t.cols % 8 == 0;
     d.tensor = uint32_t(plan.packed_tensors[pi]);
     d.lr_mult = t.lr_mult;
     std::memcpy(meta.data() + plan.off_packed_dev + pi * sizeof(PackedDev), &d, sizeof(d));
@@ -829,7 +828,6 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
     d.chunk0 = plan.norm_chunk0[i];
     d.f32 = t.dtype == MUON_F32;
     d.flat = t.rows == 1 || t.ld_grad == t.cols;
-    d.vec = d.flat || t.cols % 8 == 0;
     std::memcpy(meta.data() + plan.off_norm_dev + i * sizeof(NormDev), &d, sizeof(d));
   }
   if (plan.with_norm && !plan.chunk_tensor.empty())

@@ -211,9 +211,9 @@ struct PackedDev {
   int64_t blocks;
   int64_t value0;                      // elements of the packed tensors before this one
   int32_t f32;                         // param/grad float32 (else bf16)
-  int32_t vec;                         // groups of 8 elements are contiguous
   uint32_t tensor;                     // its place in the registered list (random words)
   float lr_mult;
+  int32_t pad;
 };
 struct PackedTask { int32_t tensor, pad; int64_t c0; };
 struct RoundingSeed { uint32_t lo, hi; };
@@ -234,7 +234,7 @@ struct NormDev {
   const void* grad;
   int64_t ld, n, cols;                 // cols: row length, of use only where flat is 0
   int64_t chunk0;                      // chunks of the tensors before this one
-  int32_t f32, flat, vec, pad;         // vec: groups of 8 elements are contiguous
+  int32_t f32, flat;                   // flat: element i lies at i
 };
 struct NormState { float norm, factor; };   // of the latest step, in the workspace
 struct NormParams {
