@@ -267,7 +267,7 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * then a 16-bit scale for each block.  A zero-filled buffer holds zeros.
  *   first moment   e4m3 number * 2^(e-127), e the block's scale: within 1/16
  *                  of the value down to 2^-14 of the block's largest, then
- *                  within 2^-18 of the largest (distances of neighbours are
+ *                  within 2^-17 of the largest (distances of neighbours are
  *                  twice that)
  *   second moment  the float32 with the bits (byte + scale) << 20, zero for
  *                  byte 0: 8 values a binade over 31 binades below the block's
@@ -286,7 +286,8 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * A first moment that is not finite stays so (NaN) and sets flag bit 0; the
  * other elements of its block are not affected.
  *
- * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35. */
+ * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35; the
+ * packed tensors of a handle hold fewer than 2^35 elements together. */
 size_t muon_packed_moment_bytes(int64_t n);
 
 /* Seed of the random rounding (0 until set); host only, from the next

@@ -47,7 +47,7 @@ constexpr int kThreads = 256;
 // A thread takes 8 elements in groups of 16 bytes of the tensor (8 of bf16, 4
 // of float32), so that a wave's access is one run of 1 KB: at half that, 32
 // bytes apart, float32 values were written back in parts (unpacking 38.6 M
-// elements 113 us with streaming stores, 67 us without, 64 us as it is now).
+// elements 113 us with streaming stores, 67 us without, 64 to 70 us as it is now).
 constexpr int kPer = 8;
 constexpr int kWave = 64 * kPer;              // elements per wave
 static_assert(kThreads * kPer == kPackChunk && kWave == 2 * kPackBlock, "a wave holds two blocks");
@@ -302,8 +302,7 @@ struct StepScalars {
 };
 
 // One group's update: w to the new weight, the moments to their new bytes.
-// `at`: the group's first element.  Returns whether a first moment is not
-// finite.
+// Returns whether a first moment is not finite.
 // PRECISE: sqrtf and division as the language has them.  Otherwise the
 // hardware's own square root and reciprocal, each within one unit in the
 // last place; that square root takes denormal numbers as zero, so it is used
@@ -473,7 +472,7 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
 //
 // HBM-bound: 10 bytes per bf16 element, 16 per float32 one: 82 M bf16 elements
 // in 128 us (6.4 TB/s), 38.6 M float32 ones in 93 us (6.6 TB/s).  The vector
-// units are busy for about 100 of the 128 us (45 instructions an element), so
+// units are busy for about 100 of the 128 us (42 instructions an element), so
 // the root and the reciprocal are the hardware's: with the language's, 65
 // instructions an element, the same took 151 us, all of them.
 // BEGINS: no launch has advanced the step count before this one.  Every wave

@@ -158,8 +158,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormParams p) {
 }  // namespace
 
 hipError_t launch_grad_norm(const NormParams& p, hipStream_t s) {
-  const int blocks = norm_blocks(p.chunks);
-  grad_norm_kernel<<<blocks > 0 ? blocks : 1, kThreads, 0, s>>>(p);   // without tensors the norm is 0
+  grad_norm_kernel<<<norm_blocks(p.chunks), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -199,7 +199,9 @@ struct Arrivals { ArriveCount group[kArriveGroups], root; };
 // formats).
 constexpr int kPackBlock = 256;
 constexpr int kPackChunk = 2048;       // elements per thread block (256 threads x 8)
-constexpr int64_t kPackMaxElems = int64_t(1) << 35;   // element / 16 fits the 32-bit counter of the random words
+// element / 16 fits the 32-bit counter of the random words, and the chunks of
+// a whole handle are a launch of at most 2^32 threads
+constexpr int64_t kPackMaxElems = int64_t(1) << 35;
 inline int64_t packed_blocks(int64_t n) { return (n + kPackBlock - 1) / kPackBlock; }
 inline int64_t packed_bytes(int64_t n) { return packed_blocks(n) * (kPackBlock + 2); }
 struct PackedDev {
@@ -229,7 +231,10 @@ struct PackedParams {
 // of n sums chunks b, b + n and so on.
 constexpr int kNormChunk = 8192;       // 256 threads x 32 elements
 constexpr int kNormBlocks = 1024;      // most blocks (and partial sums): four waves a SIMD
-inline int norm_blocks(int64_t chunks) { return static_cast<int>(chunks < kNormBlocks ? chunks : kNormBlocks); }
+// at least one: without tensors it writes the norm 0
+inline int norm_blocks(int64_t chunks) {
+  return static_cast<int>(chunks < 1 ? 1 : chunks < kNormBlocks ? chunks : kNormBlocks);
+}
 struct NormDev {
   const void* grad;
   int64_t ld, n, cols;                 // cols: row length, of use only where flat is 0

@@ -90,8 +90,11 @@ def test_refusals():
     # packed moments are AdamW's alone
     assert bad(kind=B.KIND_MUON, exp_avg_sq=None) == "MUON_ERR_UNSUPPORTED"
     big, _ = packed(1 << 15, 1 << 20)
+    assert status(big) == "MUON_ERR_UNSUPPORTED"            # 2^35 elements: 2^32 threads
     big.rows += 1
     assert status(big) == "MUON_ERR_UNSUPPORTED"
+    half, end = packed(1 << 14, 1 << 20)
+    assert status(half, packed(1 << 14, 1 << 20, end)[0]) == "MUON_ERR_UNSUPPORTED"
 
 
 def test_calls_without_a_handle():
