@@ -7,7 +7,6 @@ or cannot be loaded, every entry point raises: there is no CPU fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import json
 import os
@@ -193,9 +192,15 @@ def status_of(fn_result) -> str:
 # torch-facing wrapper (torch supplies device memory and the stream)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _as_matrix(t):
@@ -361,6 +366,7 @@ class MuonStep:
         for d in descs:
             if getattr(d, "torch_device", self.device) != self.device:
                 raise ValueError(f"a tensor on {d.torch_device} in a handle on {self.device}")
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._keep = list(keepalive)
         self._packed_elements = sum(d.rows * d.cols for d in self._descs[:self._n]
                                     if d.kind == KIND_ADAMW and d.state_bits == 8)
@@ -368,15 +374,13 @@ class MuonStep:
         h = ctypes.c_void_p()
         if static_scratch:
             self.workspace = None
-            with self._here():
-                self._check(self._lib.muon_init_static(ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
-                                                  ctypes.byref(self.hp), self._stream(None)))
+            self._launch(self._lib.muon_init_static, ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
+                         ctypes.byref(self.hp), self._stream(None))
         else:
             self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
-            with self._here():
-                self._check(self._lib.muon_init(ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
-                                           ctypes.byref(self.hp), ctypes.c_void_p(self.workspace.data_ptr()),
-                                           self.workspace.numel(), self._stream(None)))
+            self._launch(self._lib.muon_init, ctypes.byref(h), self._descs, self._n, self._pcs, self._npc,
+                         ctypes.byref(self.hp), ctypes.c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
+                         self._stream(None))
         self._h = h
 
     def _torch_stream(self, stream):
@@ -386,18 +390,21 @@ class MuonStep:
     def _stream(self, stream):
         """The hipStream_t of `stream`, or of torch's current one (asked for
         as a number where torch has that: a Stream object takes 1.5 us)."""
-        if stream is None:
-            raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-            if raw is not None:
-                return ctypes.c_void_p(raw(self.device.index))
+        if stream is None and self._raw_stream is not None:
+            return ctypes.c_void_p(self._raw_stream(self.device.index))
         return ctypes.c_void_p(self._torch_stream(stream).cuda_stream)
 
-    def _here(self):
-        """The handle's device as the current one, for a call that launches
-        kernels (HIP launches on the current device)."""
-        torch = _torch()
-        return contextlib.nullcontext() if torch.cuda.current_device() == self.device.index \
-            else torch.cuda.device(self.device)
+    def _launch(self, function, *args):
+        """Call a library function that launches kernels, with the handle's
+        device the current one (HIP launches on that)."""
+        cuda = _torch().cuda
+        if cuda.current_device() == self.device.index:
+            status = function(*args)
+        else:
+            with cuda.device(self.device):
+                status = function(*args)
+        if status != MUON_OK:
+            self._check(status)
 
     @staticmethod
     def _guard(acts, stream):
@@ -419,8 +426,7 @@ class MuonStep:
         _check(status, self._lib)
 
     def step(self, lr: float = -1.0, stream=None):
-        with self._here():
-            self._check(self._lib.muon_step(self._h, ctypes.c_float(lr), self._stream(stream)))
+        self._launch(self._lib.muon_step, self._h, lr, self._stream(stream))
 
     def step_timed(self, lr: float = -1.0, stream=None):
         """Run one step with HIP events between launches; returns
@@ -504,9 +510,7 @@ class MuonStep:
         bfloat16 tensor [2, packed_elements()]: the first moments of all packed
         tensors one after another, then the second ones (round to nearest)."""
         dt = self._check_values(values, "values")
-        s = self._stream(stream)
-        with self._here():
-            self._check(self._lib.muon_pack_moments(self._h, ctypes.c_void_p(values.data_ptr()), dt, s))
+        self._launch(self._lib.muon_pack_moments, self._h, values.data_ptr(), dt, self._stream(stream))
         if stream is not None:
             self._guard(values, stream)
 
@@ -521,9 +525,7 @@ class MuonStep:
         elif dtype is not None and dtype != out.dtype:
             raise ValueError("out is not of the dtype asked for")
         dt = self._check_values(out, "out")
-        s = self._stream(stream)
-        with self._here():
-            self._check(self._lib.muon_unpack_moments(self._h, ctypes.c_void_p(out.data_ptr()), dt, s))
+        self._launch(self._lib.muon_unpack_moments, self._h, out.data_ptr(), dt, self._stream(stream))
         if stream is not None:
             self._guard(out, stream)
         return out
