@@ -370,6 +370,9 @@ class MuonStep:
         self._keep = list(keepalive)
         self._packed_elements = sum(d.rows * d.cols for d in self._descs[:self._n]
                                     if d.kind == KIND_ADAMW and d.state_bits == 8)
+        # a captured step goes on writing here after the norm is switched off,
+        # so the buffer lives as long as the handle
+        self._norm_out = torch.zeros(2, device=self.device)
         self.grad_norm = None
         h = ctypes.c_void_p()
         if static_scratch:
@@ -481,10 +484,7 @@ class MuonStep:
         following step (float('inf'): measure only; 0: off).  `grad_norm` is
         then a device tensor that each step fills with (norm, factor); it is
         None while off."""
-        torch = _torch()
-        out = None
-        if max_norm > 0:
-            out = self.grad_norm if self.grad_norm is not None else torch.zeros(2, device=self.device)
+        out = self._norm_out if max_norm > 0 else None
         self._check(self._lib.muon_set_max_grad_norm(self._h, ctypes.c_float(max_norm),
                                                 ctypes.c_void_p(out.data_ptr() if out is not None else None)))
         self.grad_norm = out

@@ -204,3 +204,29 @@ def test_refusals():
     empty.step()
     assert empty.grad_norm.tolist() == [0.0, 1.0]
     empty.close()
+
+
+def test_norm_of_a_captured_step_outlives_the_setting():
+    say("case: a captured clipped step replayed after clipping was switched off")
+    a, b = Mixed("bf16"), Mixed("bf16")
+    sa, sb = mm.MuonStep(a.descs()), mm.MuonStep(b.descs())
+    for s in (sa, sb):
+        s.set_max_grad_norm(0.5)
+    place = sb.grad_norm.data_ptr()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        sb.step()
+    sb.set_max_grad_norm(0.0)
+    others = [torch.zeros(2, device="cuda") for _ in range(64)]
+    assert place not in [x.data_ptr() for x in others]
+    for _ in range(3):
+        sa.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(a.state(), b.state()))
+        assert not any(bool(x.any()) for x in others)
+    sb.set_max_grad_norm(0.5)                    # on again: the same place, with the replays' figures
+    assert sb.grad_norm.data_ptr() == place and torch.equal(sa.grad_norm, sb.grad_norm)
+    sa.close()
+    sb.close()
