@@ -520,14 +520,20 @@ class MuonStep:
         float32), laid out as pack_moments takes it; into `out` if given.
         split_moments cuts it into the tensors' own."""
         torch = _torch()
-        if out is None:
+        given = out is not None
+        if given:
+            if dtype is not None and dtype != out.dtype:
+                raise ValueError("out is not of the dtype asked for")
+        elif stream is not None:
+            # of that stream's memory: a block of the current one may still be in use there
+            with torch.cuda.stream(stream):
+                out = torch.empty((2, self._packed_elements), dtype=dtype or torch.float32, device=self.device)
+        else:
             out = torch.empty((2, self._packed_elements), dtype=dtype or torch.float32, device=self.device)
-        elif dtype is not None and dtype != out.dtype:
-            raise ValueError("out is not of the dtype asked for")
         dt = self._check_values(out, "out")
         self._launch(self._lib.muon_unpack_moments, self._h, out.data_ptr(), dt, self._stream(stream))
         if stream is not None:
-            self._guard(out, stream)
+            self._guard(out, stream if given else torch.cuda.current_stream(self.device))
         return out
 
     def split_moments(self, values):

@@ -471,3 +471,22 @@ def test_static_scratch():
         x.check(t, 0, hp)
     assert st.grad_norm[1].item() == 1.0
     st.close()
+
+
+def test_unpack_on_another_stream_takes_that_streams_memory():
+    say("case: unpacking on a side stream while the current stream still uses a freed block")
+    x = Packed((330,), (64, 4096), "bf16")
+    st = mm.MuonStep([x.desc()])
+    x.grad(1)
+    st.step()
+    want = st.unpack_moments().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    block = torch.zeros_like(want)
+    place = block.data_ptr()
+    del block                                    # the current stream may hand it out again, another one not
+    got = st.unpack_moments(stream=side)
+    assert got.data_ptr() != place
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    st.close()
