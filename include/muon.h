@@ -311,9 +311,11 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
  * computes norm = sqrt(sum of the squares of every registered gradient, Muon
  * and AdamW) in float64 and multiplies each gradient by
  * min(1, max_norm / norm) as it reads it; the gradients in memory stay as they
- * are.  INFINITY measures without clipping, 0 (the default) switches both off.
- * A gradient that is not finite makes the norm so, and with it the factor: NaN
- * for NaN, 0 for an infinite norm (whose infinite gradients become NaN).
+ * are.  INFINITY measures without clipping (the factor is always 1), 0 (the
+ * default) switches both off.
+ * A gradient that is not finite makes the norm so, and with a finite max_norm
+ * the factor: NaN for NaN, 0 for an infinite norm (whose infinite gradients
+ * become NaN).
  * norm_out: NULL, or device memory for two floats that each step fills with
  * (norm, factor) on its stream; it must live as long as it is set.  Host only;
  * a captured step keeps what was set when it was captured.  A handle of

@@ -1,7 +1,7 @@
 // Global gradient norm and clipping factor of one step:
 //
 //   norm = sqrt(sum over every registered gradient of g^2),
-//   factor = min(1, max_norm / norm)
+//   factor = min(1, max_norm / norm), always 1 with an infinite max_norm
 //
 // The gradients are read only; the kernels that read them next multiply by
 // the factor as they do.  Squares and sums are float64: no overflow for any
@@ -121,8 +121,10 @@ __device__ __forceinline__ void finish(const NormParams& p, int blocks, double* 
   s = block_sum64(s, red);
   if (threadIdx.x == 0) {
     const double norm = sqrt(s);
-    // a NaN among the gradients makes the norm, and so every gradient, NaN
-    const float factor = norm <= p.max_norm ? 1.f : static_cast<float>(p.max_norm / norm);
+    // a NaN among the gradients makes the norm, and so every gradient, NaN,
+    // but for a norm that is only measured
+    const bool keep = norm <= p.max_norm || p.max_norm == INFINITY;
+    const float factor = keep ? 1.f : static_cast<float>(p.max_norm / norm);
     p.state->norm = static_cast<float>(norm);
     p.state->factor = factor;
     if (p.norm_out) {

@@ -115,6 +115,6 @@ def clip(grads, max_norm):
     """(norm, factor) of a list of gradients."""
     with np.errstate(all="ignore"):
         norm = float(np.sqrt(sum(float(np.sum(np.asarray(g, np.float64) ** 2)) for g in grads)))
-    if norm <= max_norm:
+    if norm <= max_norm or max_norm == np.inf:
         return norm, 1.0
     return norm, max_norm / norm

@@ -230,3 +230,24 @@ def test_norm_of_a_captured_step_outlives_the_setting():
     assert sb.grad_norm.data_ptr() == place and torch.equal(sa.grad_norm, sb.grad_norm)
     sa.close()
     sb.close()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_measuring_does_not_spread_a_bad_gradient(bad):
+    say(f"case: measured, not clipped, with a gradient of {bad}: bitwise the plain step")
+    a, b = Mixed("f32"), Mixed("f32")
+    for x in (a, b):
+        x.grads()[4][3] = bad                    # one element of a packed tensor
+    sa, sb = mm.MuonStep(a.descs()), mm.MuonStep(b.descs())
+    sa.set_max_grad_norm(float("inf"))
+    for s in (sa, sb):
+        s.step()
+    norm, factor = sa.grad_norm.tolist()
+    assert factor == 1.0 and (norm != norm if bad != bad else norm == bad)
+    for p, q in zip(a.state(), b.state()):
+        assert torch.equal(p.contiguous().view(torch.uint8), q.contiguous().view(torch.uint8))
+    assert sa.flags() == sb.flags() == 1
+    w = a.sets[4][1]
+    assert bool(w[3].isnan()) and int(w.isnan().sum()) == 1
+    sa.close()
+    sb.close()

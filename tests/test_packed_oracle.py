@@ -187,3 +187,10 @@ def test_clip_factor():
     assert pm.clip(g, 1.0) == (5.0, 0.2)
     assert np.isnan(pm.clip([np.array([np.nan])], 1.0)[1])
     assert pm.clip([np.array([np.inf])], 1.0) == (np.inf, 0.0)
+
+
+def test_measuring_leaves_the_factor_at_one():
+    for g, norm in (([3.0, 4.0], 5.0), ([np.inf], np.inf)):
+        assert pm.clip([np.array(g)], np.inf) == (norm, 1.0)
+    norm, factor = pm.clip([np.array([1.0, np.nan])], np.inf)
+    assert np.isnan(norm) and factor == 1.0
