@@ -371,8 +371,11 @@ class MuonStep:
         self._packed_elements = sum(d.rows * d.cols for d in self._descs[:self._n]
                                     if d.kind == KIND_ADAMW and d.state_bits == 8)
         # a captured step goes on writing here after the norm is switched off,
-        # so the buffer lives as long as the handle
-        self._norm_out = torch.zeros(2, device=self.device)
+        # so the buffer lives as long as the handle; it is there from the start,
+        # like the workspace, so that its zeros precede steps on any stream
+        # that follows the init.  A static handle allocates nothing until it is
+        # asked for the norm.
+        self._norm_out = None if static_scratch else torch.zeros(2, device=self.device)
         self.grad_norm = None
         h = ctypes.c_void_p()
         if static_scratch:
@@ -484,6 +487,8 @@ class MuonStep:
         following step (float('inf'): measure only; 0: off).  `grad_norm` is
         then a device tensor that each step fills with (norm, factor); it is
         None while off."""
+        if max_norm > 0 and self._norm_out is None:
+            self._norm_out = _torch().zeros(2, device=self.device)
         out = self._norm_out if max_norm > 0 else None
         self._check(self._lib.muon_set_max_grad_norm(self._h, ctypes.c_float(max_norm),
                                                 ctypes.c_void_p(out.data_ptr() if out is not None else None)))

@@ -251,3 +251,21 @@ def test_measuring_does_not_spread_a_bad_gradient(bad):
     assert bool(w[3].isnan()) and int(w.isnan().sum()) == 1
     sa.close()
     sb.close()
+
+
+def test_static_handle_allocates_at_the_first_setting():
+    say("case: norm of a static handle, no torch memory before it is set")
+    x = Packed((340,), (500,), "f32")
+    x.grad(1)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    st = mm.MuonStep([x.desc()], static_scratch=True)
+    assert torch.cuda.memory_allocated() == before and st.grad_norm is None
+    st.set_max_grad_norm(0.5)
+    place = st.grad_norm.data_ptr()
+    st.step()
+    _close(st.grad_norm, *_ref([x.dG], 0.5))
+    st.set_max_grad_norm(0.0)
+    st.set_max_grad_norm(float("inf"))
+    assert st.grad_norm.data_ptr() == place
+    st.close()
