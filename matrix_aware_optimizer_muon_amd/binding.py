@@ -486,9 +486,19 @@ class MuonStep:
         """Clip by the global norm of all registered gradients in every
         following step (float('inf'): measure only; 0: off).  `grad_norm` is
         then a device tensor that each step fills with (norm, factor); it is
-        None while off."""
+        None while off.  A static handle allocates it the first time it is
+        switched on, which synchronises the current stream and is refused
+        while that is being captured."""
         if max_norm > 0 and self._norm_out is None:
-            self._norm_out = _torch().zeros(2, device=self.device)
+            torch = _torch()
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the norm of a static handle is set for the first time before a capture: "
+                                   "its buffer must not belong to the captured graph")
+            norm_out = torch.zeros(2, device=self.device)
+            # a step on any stream may write it from now on: after the zeros, and after whatever the current
+            # stream last did with that memory
+            torch.cuda.current_stream(self.device).synchronize()
+            self._norm_out = norm_out
         out = self._norm_out if max_norm > 0 else None
         self._check(self._lib.muon_set_max_grad_norm(self._h, ctypes.c_float(max_norm),
                                                 ctypes.c_void_p(out.data_ptr() if out is not None else None)))

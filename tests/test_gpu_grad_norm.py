@@ -269,3 +269,24 @@ def test_static_handle_allocates_at_the_first_setting():
     st.set_max_grad_norm(float("inf"))
     assert st.grad_norm.data_ptr() == place
     st.close()
+
+
+def test_static_handle_norm_set_on_a_busy_stream():
+    say("case: norm of a static handle set on a stream with work in flight, the step on another one")
+    x = Packed((350,), (500,), "f32")
+    x.grad(1)
+    torch.cuda.synchronize()
+    st = mm.MuonStep([x.desc()], static_scratch=True)
+    busy = torch.zeros(1 << 26, device="cuda")
+    for _ in range(50):
+        busy.add_(1.0)
+    st.set_max_grad_norm(0.5)
+    side = torch.cuda.Stream()
+    st.step(stream=side)
+    side.synchronize()
+    norm, factor = _ref([x.dG], 0.5)
+    _close(st.grad_norm, norm, factor)
+    torch.cuda.synchronize()
+    _close(st.grad_norm, norm, factor)
+    assert bool((busy == 50).all())
+    st.close()
