@@ -286,8 +286,9 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * A first moment that is not finite stays so (NaN) and sets flag bit 0; the
  * other elements of its block are not affected.
  *
- * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35; the
- * packed tensors of a handle hold fewer than 2^35 elements together. */
+ * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35.  The
+ * packed tensors of one handle make at most 2^24 - 1 chunks of 2048 elements
+ * together, each tensor's last one counted whole (about 2^35 elements). */
 size_t muon_packed_moment_bytes(int64_t n);
 
 /* Seed of the random rounding (0 until set); host only, from the next

@@ -482,10 +482,10 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   plan.apply_bf16 = int(plan.apply.size());
   plan.apply.insert(plan.apply.end(), apply_f32.begin(), apply_f32.end());
   std::vector<PackedTask> packed_by_kind[kPackKinds];
-  int64_t packed_all = 0;
+  int64_t packed_chunks = 0;
   for (int32_t i = 0; i < n; ++i)
-    if (packed(ts[i])) packed_all += ts[i].rows * ts[i].cols;
-  if (packed_all >= kPackMaxElems)            // in chunks, a launch of fewer than 2^32 threads
+    if (packed(ts[i])) packed_chunks += (ts[i].rows * ts[i].cols + kPackChunk - 1) / kPackChunk;
+  if (packed_chunks > kPackMaxChunks)
     return fail(MUON_ERR_UNSUPPORTED, "too many elements with 8-bit moments for one handle");
   // AdamW tensors: rows of `len` elements in chunks of kAdamChunk; a fully
   // contiguous tensor is one row of rows*cols elements

@@ -199,9 +199,12 @@ struct Arrivals { ArriveCount group[kArriveGroups], root; };
 // formats).
 constexpr int kPackBlock = 256;
 constexpr int kPackChunk = 2048;       // elements per thread block (256 threads x 8)
-// element / 16 fits the 32-bit counter of the random words, and the chunks of
-// a whole handle are a launch of at most 2^32 threads
+// element / 16 of a tensor fits the 32-bit counter of the random words
 constexpr int64_t kPackMaxElems = int64_t(1) << 35;
+// of a whole handle, each tensor's last chunk counted whole: a launch of all
+// of them stays below 2^32 threads
+constexpr int64_t kPackMaxChunks = (int64_t(1) << 24) - 1;
+static_assert((kPackMaxChunks + 1) * 256 == int64_t(1) << 32, "256 threads a chunk");
 inline int64_t packed_blocks(int64_t n) { return (n + kPackBlock - 1) / kPackBlock; }
 inline int64_t packed_bytes(int64_t n) { return packed_blocks(n) * (kPackBlock + 2); }
 struct PackedDev {

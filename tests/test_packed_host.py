@@ -122,3 +122,32 @@ def test_descriptor_from_tensors():
             mm.adam_tensor_desc(*bad)
     f = torch.zeros(30, 20)
     assert mm.adam_tensor_desc(p, g, f, f.clone()).state_bits == 0
+
+
+MOST_CHUNKS = (1 << 24) - 1          # 2^24 blocks of 256 threads are 2^32, one launch's limit
+LARGE = ((1 << 20) - 1, 1 << 15)     # 2^24 - 16 chunks
+
+
+def many(shapes):
+    ts, end = [], BASE
+    for r, c in shapes:
+        t, end = packed(r, c, end)
+        ts.append(t)
+    return ts
+
+
+@pytest.mark.parametrize("shapes", [[LARGE, (15, 2048)], [LARGE, (13, 2048), (1, 1), (1, 2047)]])
+def test_most_chunks_of_a_handle(shapes):
+    assert sum(-(-r * c // 2048) for r, c in shapes) == MOST_CHUNKS
+    assert status(*many(shapes)) == "MUON_OK"
+
+
+@pytest.mark.parametrize("shapes", [
+    [LARGE, (1, (1 << 15) - 1)],                              # 2^35 - 1 elements, 2^24 chunks
+    [LARGE, (15, 2048), (1, 1)],                              # a chunk for one element
+    [LARGE, (12, 2048), *[(1, k) for k in (1, 2, 255, 2047)]],
+])
+def test_too_many_chunks_are_refused(shapes):
+    assert sum(r * c for r, c in shapes) < 1 << 35
+    assert sum(-(-r * c // 2048) for r, c in shapes) > MOST_CHUNKS
+    assert status(*many(shapes)) == "MUON_ERR_UNSUPPORTED"
