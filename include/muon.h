@@ -266,9 +266,9 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * holds the bytes of the row-major elements, filled up to whole blocks of 256,
  * then a 16-bit scale for each block.  A zero-filled buffer holds zeros.
  *   first moment   e4m3 number * 2^(e-127), e the block's scale: within 1/16
- *                  of the value down to 2^-14 of the block's largest, then
- *                  within 2^-17 of the largest (distances of neighbours are
- *                  twice that)
+ *                  of the value down to 2^-13 of the block's largest, then
+ *                  within 2^-17 of the largest (or 2^-128, where that is more);
+ *                  distances of neighbours are twice that
  *   second moment  the float32 with the bits (byte + scale) << 20, zero for
  *                  byte 0: 8 values a binade over 31 binades below the block's
  *                  largest; smaller ones are raised to the smallest value, and

@@ -13,7 +13,7 @@
 // Bytes.  A block is 256 consecutive elements of the row-major tensor.
 //   first moment   an OCP e4m3 number times 2^(e-127), one e for each block,
 //                  the smallest (from 9 on) that brings the block's largest
-//                  magnitude to 448 or below.  Above 2^-14 of the largest,
+//                  magnitude to 448 or below.  Above 2^-13 of the largest,
 //                  neighbouring values are 6 to 12 % apart; below it they
 //                  run linearly to zero.
 //   second moment  never negative, so all 8 bits are magnitude: the float32

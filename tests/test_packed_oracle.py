@@ -5,6 +5,7 @@ states, the mean of the random rounding, and planted mistakes."""
 import numpy as np
 import pytest
 
+from matrix_aware_optimizer_muon_amd.binding import HEADER_PATH
 from oracle import packed_moments as pm
 
 torch = pytest.importorskip("torch")
@@ -194,3 +195,42 @@ def test_measuring_leaves_the_factor_at_one():
         assert pm.clip([np.array(g)], np.inf) == (norm, 1.0)
     norm, factor = pm.clip([np.array([1.0, np.nan])], np.inf)
     assert np.isnan(norm) and factor == 1.0
+
+
+with open(HEADER_PATH) as f:
+    HEADER = f.read()
+
+
+@pytest.mark.parametrize("top", [224.0, 224.01, 300.0, 447.99, 448.0])
+@pytest.mark.parametrize("exponent", [-100, -20, 3])
+def test_first_moment_bound_as_the_header_states_it(top, exponent):
+    # include/muon.h: within 1/16 of the value down to 2^-13 of the block's largest, then within 2^-17 of the
+    # largest.  The largest may be any number of (224, 448] units, and e4m3 is subnormal below 2^-6 units.
+    assert "within 1/16\n *                  of the value down to 2^-13 of the block's largest, then\n" \
+        " *                  within 2^-17 of the largest" in HEADER
+    rng = _rng(20, int(top * 100), exponent + 200)
+    big = np.float32(top * 2.0 ** exponent)
+    near = 2.0 ** -13 * (1 + np.concatenate([rng.uniform(-1e-3, 1e-3, 2000), rng.uniform(-0.5, 1.0, 4000)]))
+    share = np.concatenate([near, 10.0 ** rng.uniform(-12, 0, 8000)])
+    m = (share * float(big)).astype(np.float32) * rng.choice([-1, 1], share.size).astype(np.float32)
+    m[::pm.BLOCK] = big
+    dm, _ = pm.decode(*pm.encode(m, np.zeros_like(m)), m.size)
+    err, size = np.abs(dm - m), np.abs(m.astype(np.float64))
+    held = size >= 2.0 ** -13 * float(big)
+    assert (err <= size / 16)[held].all() and (err <= 2.0 ** -17 * float(big))[~held].all()
+    # not from 2^-14 on: a largest just above 224 units leaves 2^-13.8 of it subnormal
+    if top == 224.01:
+        x = np.zeros(pm.BLOCK, np.float32)
+        x[0], x[1] = big, np.float32(1.072 * 2.0 ** -14 * float(big))
+        assert abs(pm.decode(*pm.encode(x, np.zeros_like(x)), pm.BLOCK)[0][1] - x[1]) > x[1] / 16
+
+
+def test_first_moment_bound_of_tiny_blocks():
+    # ... or within 2^-128, where that is more: the scales end at 2^(9-127)
+    assert "(or 2^-128, where that is more)" in HEADER
+    m = (_rng(21).normal(0, 1, 4096) * 2.0 ** _rng(22).uniform(-125, -112, 4096)).astype(np.float32)
+    dm, _ = pm.decode(*pm.encode(m, np.zeros_like(m)), m.size)
+    big = np.abs(m.reshape(-1, pm.BLOCK)).max(1).repeat(pm.BLOCK).astype(np.float64)
+    bound = np.where(np.abs(m) >= 2.0 ** -13 * big, np.abs(m.astype(np.float64)) / 16, 2.0 ** -17 * big)
+    assert (np.abs(dm - m) <= np.maximum(bound, 2.0 ** -128)).all()
+    assert (np.abs(dm - m) > bound).any()
