@@ -284,7 +284,10 @@ muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_t
  * first at beta1 = 0.9 by 8 % of its rms, and m / sqrt(v) by 10 to 13 % of its
  * own.
  * A first moment that is not finite stays so (NaN) and sets flag bit 0; the
- * other elements of its block are not affected.
+ * other elements of its block are not affected.  A finite first moment above
+ * 1.875 * 2^127 in magnitude is held as that, and so is a second moment above
+ * it, an infinite one too (of a gradient whose square overflows, or given to
+ * muon_pack_moments), without a flag.
  *
  * muon_packed_moment_bytes returns 0 for a count below 1 or above 2^35.  The
  * packed tensors of one handle make at most 2^24 - 1 chunks of 2048 elements

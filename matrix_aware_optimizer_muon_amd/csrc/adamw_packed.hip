@@ -34,7 +34,9 @@
 // The conversion from values rounds to nearest, ties to even.
 //
 // A first moment that is not finite becomes e4m3's NaN and takes no part in
-// its block's scales; its second moment's byte is then without meaning.
+// its block's scales; its second moment's byte is then without meaning.  What
+// is above 1.875 * 2^127 is held as that, in either moment: the next values
+// up, 2^128, are infinite as float32.
 #include <cmath>
 
 #include "device_common.h"
@@ -57,7 +59,8 @@ constexpr int kWordGroup = 16;                // elements that share a hash
 template <int W> using codes_t = unsigned int __attribute__((ext_vector_type(W / 4)));
 
 constexpr uint32_t kInf = 0x7F800000u;
-constexpr uint32_t kSecondMost = 0x7F700000u; // 1.875 * 2^127, the largest second moment a byte stands for
+constexpr uint32_t kMost = 0x7F700000u;       // 1.875 * 2^127, the largest magnitude a byte stands for
+constexpr uint32_t kScaleMost = 247;          // of a block with a first moment above 1.75 * 2^127
 constexpr uint32_t kScaleLeast = 9;           // keeps e4m3's smallest value times the scale exact in bf16
 
 // Maximum over the lanes that hold a block (W elements each): rotations within
@@ -128,6 +131,18 @@ struct Packed {
       gst(d.m_scales + i / kPackBlock, static_cast<uint16_t>(s.e));
       gst(d.v_scales + i / kPackBlock, static_cast<uint16_t>(s.base));
     }
+    // 256 units (code 0x78) of the largest scale are 2^128: 240 (0x77) in their
+    // place.  Stored once more, as a correction before the first store kept the
+    // weights in registers past it: up to 9 spilled of 64.
+    if (s.e == kScaleMost) {
+      codes_t<W> x = m;
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const uint32_t apart = (x[q] & 0x7F7F7F7Fu) ^ 0x78787878u;   // byte by byte, zero where the code is 0x78
+        x[q] -= ((0x80808080u - apart) & 0x80808080u) >> 7;
+      }
+      gst_nt(d.m + i, x);
+    }
   }
   __device__ __forceinline__ void decode(float* mo, float* vo) const {
     const float scale = __uint_as_float(max(s.e, kScaleLeast) << 23);   // a zero-filled buffer has no scales
@@ -164,13 +179,13 @@ __device__ __forceinline__ bool Packed<W>::encode(const float* mi, float* vi, ui
   }
   const bool bad = mx >= kInf;
   uint32_t m_top = block_max<W>(mx), v_top = block_max<W>(vx);
-  const bool odd = m_top >= kInf || v_top > kSecondMost;   // the same in all lanes of a block
+  const bool odd = m_top >= kInf || v_top > kMost;   // the same in all lanes of a block
   if (odd) {                       // leave non-finite elements out, bound the second moments
     mx = vx = 0;
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       const uint32_t a = __float_as_uint(mi[e]) & 0x7FFFFFFFu;
-      const uint32_t b = a < kInf ? min(__float_as_uint(vi[e]), kSecondMost) : 0u;
+      const uint32_t b = a < kInf ? min(__float_as_uint(vi[e]), kMost) : 0u;
       mx = max(mx, a < kInf ? a : 0u);
       vx = max(vx, b);
       vi[e] = __uint_as_float(b);

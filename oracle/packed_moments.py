@@ -13,7 +13,7 @@ import numpy as np
 BLOCK = 256
 GOLDEN, ROOT3 = np.uint32(0x9E3779B9), np.uint32(0xBB67AE85)
 F32_INF = 0x7F800000
-SECOND_MOST = 0x7F700000
+MOST = 0x7F700000              # 1.875 * 2^127, the largest magnitude a byte stands for
 SCALE_LEAST = 9
 
 # e4m3 (OCP): 4 exponent bits of bias 7, 3 mantissa bits, subnormals, no
@@ -56,8 +56,8 @@ def encode(m, v, word=None):
     nb = m.shape[0]
     w = None if word is None else _blocks(np.asarray(word, np.uint32)).astype(np.int64)
     ok = np.isfinite(m)
-    mag = np.where(ok, np.abs(m), np.float32(0))
-    vbits = np.minimum((v.view(np.uint32) & 0x7FFFFFFF).astype(np.int64), SECOND_MOST)
+    mag = np.minimum(np.where(ok, np.abs(m), np.float32(0)), np.float32(1.875 * 2.0 ** 127))
+    vbits = np.minimum((v.view(np.uint32) & 0x7FFFFFFF).astype(np.int64), MOST)
     vbits[~ok] = 0
     # first moment
     top = mag.max(1).view(np.uint32).astype(np.int64)

@@ -490,3 +490,31 @@ def test_unpack_on_another_stream_takes_that_streams_memory():
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want)
     st.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_first_moments_stay_finite(dtype):
+    say(f"case: {dtype} first moments up to the type's largest, packed and stepped, against the oracle")
+    tt = torch.float32 if dtype == "f32" else torch.bfloat16
+    most, top = 1.875 * 2.0 ** 127, torch.finfo(tt).max
+    x = Packed((360,), (1000,), dtype)
+    hp = mm.default_hparams(adam_beta1=0.0, adam_beta2=0.5)       # the first moment is the gradient
+    st = mm.MuonStep([x.desc()], hp)
+    big = _rng(361).uniform(1.7 * 2.0 ** 127, top, 1000) * _rng(362).choice([-1, 1], 1000)
+    big[:6] = most, -top, top, 1.9375 * 2.0 ** 127, 1e30, 0.0
+    m = _store(big, dtype)
+    m64 = _decode(m, dtype)
+    v = _store(np.full(1000, 1e-8), dtype)
+    st.pack_moments(torch.stack([to_device(torch, m, dtype), to_device(torch, v, dtype)]))
+    x.mem = pm.encode(m64.astype(np.float32), _decode(v, dtype).astype(np.float32))
+    assert _same_bytes(x.dM.cpu().numpy(), x.mem[0], 1000, True)
+    out = st.unpack_moments(tt)[0].double().cpu().numpy()
+    assert np.array_equal(out, pm.decode(*x.mem, 1000)[0]) and np.abs(out).max() == most
+    # gradients of that size step the same way: random rounding, the second moments overflow
+    x.set_grad(m64.reshape(1, 1000))
+    st.step()
+    x.check(1, 0, hp)
+    out = st.unpack_moments(torch.float32)
+    assert bool(out.isfinite().all()) and out[0].abs().max().item() == most
+    assert out[1].max().item() == most and st.flags() == 0
+    st.close()

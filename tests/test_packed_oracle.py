@@ -234,3 +234,17 @@ def test_first_moment_bound_of_tiny_blocks():
     bound = np.where(np.abs(m) >= 2.0 ** -13 * big, np.abs(m.astype(np.float64)) / 16, 2.0 ** -17 * big)
     assert (np.abs(dm - m) <= np.maximum(bound, 2.0 ** -128)).all()
     assert (np.abs(dm - m) > bound).any()
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "random"])
+def test_largest_first_moments_stay_finite(rounding):
+    # 448 * 2^120 is no float32: what lies above 1.875 * 2^127 is held as that, within 1/16 of it
+    most, f32_max = 1.875 * 2.0 ** 127, float(np.finfo(np.float32).max)
+    m = np.concatenate([_rng(23).uniform(1.7 * 2.0 ** 127, f32_max, 2000), [most, 1.9375 * 2.0 ** 127, f32_max, -f32_max],
+                        np.full(44, 1e30)]).astype(np.float32)
+    word = None if rounding == "nearest" else pm.words(3, 1, 0, m.size)
+    dm, _ = pm.decode(*pm.encode(m, np.zeros_like(m), word), m.size)
+    assert np.isfinite(dm.astype(np.float32)).all() and np.abs(dm).max() == most
+    over = np.abs(m) >= most
+    assert over.sum() > 500 and (dm[over] == np.copysign(most, m[over])).all()
+    assert (np.abs(dm - m.astype(np.float64))[over] <= np.abs(m.astype(np.float64))[over] / 16).all()
