@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import json
+import math
 import os
 import re
 from typing import List, Optional, Sequence
@@ -489,6 +490,10 @@ class MuonStep:
         None while off.  A static handle allocates it the first time it is
         switched on, which synchronises the current stream and is refused
         while that is being captured."""
+        max_norm = float(max_norm)
+        held = ctypes.c_float(max_norm).value         # what the library gets
+        if (held == 0) != (max_norm == 0) or math.isinf(held) != math.isinf(max_norm):
+            raise ValueError(f"a maximum norm is 0, infinite, or a number that float32 holds as neither: {max_norm}")
         if max_norm > 0 and self._norm_out is None:
             torch = _torch()
             if torch.cuda.is_current_stream_capturing():

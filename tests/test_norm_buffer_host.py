@@ -1,5 +1,5 @@
-"""Host-only checks of how the binding keeps the gradient norm's buffer (no
-GPU): a recording stand-in for torch and for the library."""
+"""Host-only checks of how the binding sets the gradient norm and keeps its
+buffer (no GPU): a recording stand-in for torch and for the library."""
 
 import ctypes
 import types
@@ -64,4 +64,24 @@ def test_first_setting_is_refused_under_capture(monkeypatch):
     st, events = step_object(monkeypatch, norm_out=torch.zeros(2), capturing=True)
     st.set_max_grad_norm(0.5)
     assert events == [("set", 0.5, True)]
+    st._h = None
+
+
+@pytest.mark.parametrize("max_norm", [1e-50, -1e-50, 1e39, 3.5e38, 10 ** 60])
+def test_norms_that_float32_does_not_hold_are_refused(monkeypatch, max_norm):
+    # the library would read 1e-50 as "off" and 1e39 as "measure only"
+    st, events = step_object(monkeypatch, norm_out=torch.zeros(2))
+    with pytest.raises(ValueError):
+        st.set_max_grad_norm(max_norm)
+    assert events == [] and st.grad_norm is None
+    st._h = None
+
+
+@pytest.mark.parametrize("max_norm,on", [(0, False), (0.0, False), (1e-45, True), (2.0 ** -126, True), (3, True),
+                                         (3.4e38, True), (float("inf"), True), (torch.tensor(0.25), True)])
+def test_norms_that_float32_holds_are_set(monkeypatch, max_norm, on):
+    st, events = step_object(monkeypatch, norm_out=torch.zeros(2))
+    st.set_max_grad_norm(max_norm)
+    assert events == [("set", ctypes.c_float(float(max_norm)).value, on)]
+    assert (st.grad_norm is not None) == on == (events[0][1] > 0)
     st._h = None
