@@ -244,7 +244,9 @@ muon_status_t muon_step(muon_handle_t h, float lr, void* stream);
  * milliseconds of phase i (see muon_phase_name) and *n_phases their count
  * (at most max_phases are written).  Every launch runs on `stream`, one
  * after the other (no lanes), so each phase's time is that launch's alone.
- * For profiling only. */
+ * For profiling only.  With a maximum norm set (muon_set_max_grad_norm) phase 0
+ * is the norm's, "grad_norm", and the others come one later.  A name stays
+ * where it is until muon_destroy(). */
 muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream,
                               float* phase_ms, int32_t max_phases, int32_t* n_phases);
 const char* muon_phase_name(muon_handle_t h, int32_t phase);

@@ -857,7 +857,7 @@ struct muon_handle_s {
   hipEvent_t ev_aux = nullptr, ev_adam = nullptr;
   hipEvent_t ev_fork = nullptr;
   std::vector<hipEvent_t> events;
-  std::vector<std::string> phase_names;
+  std::vector<std::string> phase_names;   // fixed at init; the norm's phase, where it is on, comes before them
   float max_norm = 0.f;          // > 0: every step clips by the global gradient norm
   float* norm_out = nullptr;     // where the caller wants the norm and the factor, or NULL
   uint64_t rounding_seed = 0;
@@ -866,6 +866,9 @@ struct muon_handle_s {
 };
 
 namespace {
+
+// Phases of the gradient norm, before the others.
+int32_t norm_phases(muon_handle_t h) { return h->max_norm > 0.f ? 1 : 0; }
 
 // Enqueue one whole step.  With `ev` non-null, record ev[k] before launch k
 // and ev[last] after the final one.
@@ -1458,7 +1461,7 @@ muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream, float* ph
   if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
   if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
   if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  const size_t np = h->phase_names.size();
+  const size_t np = size_t(norm_phases(h)) + h->phase_names.size();
   if (h->events.size() < np + 1) {
     while (h->events.size() < np + 1) {
       hipEvent_t ev;
@@ -1482,8 +1485,10 @@ muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream, float* ph
 }
 
 const char* muon_phase_name(muon_handle_t h, int32_t phase) {
-  if (!h || phase < 0 || size_t(phase) >= h->phase_names.size()) return "";
-  return h->phase_names[size_t(phase)].c_str();
+  if (!h || phase < 0) return "";
+  if (phase < norm_phases(h)) return "grad_norm";
+  const size_t k = size_t(phase - norm_phases(h));
+  return k < h->phase_names.size() ? h->phase_names[k].c_str() : "";
 }
 
 muon_status_t muon_set_adam_step(muon_handle_t h, int64_t steps_taken, void* stream) {
@@ -1531,9 +1536,6 @@ muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* nor
       const muon_status_t st = check_apart(h, norm_out, 2 * sizeof(float), "norm_out");
       if (st != MUON_OK) return st;
     }
-    const bool was = h->max_norm > 0.f, is = max_norm > 0.f;
-    if (is && !was) h->phase_names.insert(h->phase_names.begin(), "grad_norm");
-    if (was && !is) h->phase_names.erase(h->phase_names.begin());
     h->max_norm = max_norm;
     h->norm_out = norm_out;
     return MUON_OK;

@@ -1,0 +1,43 @@
+"""The handle's host code where the host runs out of memory, where a HIP call
+fails, and where the gradient norm is switched on and off (CPU only):
+`muon_host.cpp` with stand-ins for the HIP runtime and the kernel launchers
+(`tests/host_handle/driver.cpp`), an operator new that fails on request, and
+counts of what lives."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from matrix_aware_optimizer_muon_amd import build as BLD
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+
+
+def _run(cmd):
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    assert r.returncode == 0, r.stdout[-4000:]
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    if not os.path.exists(HIPCC):
+        pytest.skip("needs hipcc")
+    d = tmp_path_factory.mktemp("handle")
+    objs = []
+    for src in (os.path.join(BLD.CSRC, "muon_host.cpp"), os.path.join(HERE, "host_handle", "driver.cpp")):
+        objs.append(str(d / (os.path.splitext(os.path.basename(src))[0] + ".o")))
+        _run([HIPCC, f"--offload-arch={BLD.ARCH}", "-O1", "-fPIC", "-std=c++17", "-x", "hip",
+              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+              f"-I{BLD.INCLUDE}", f"-I{BLD.CSRC}", "-c", src, "-o", objs[-1]])
+    exe = str(d / "handle")
+    _run([HIPCC, f"--offload-arch={BLD.ARCH}", *objs, *BLD.LINK_FLAGS, "-o", exe])
+    return exe
+
+
+@pytest.mark.parametrize("what", ["names"])
+def test_handle(driver, what):
+    r = subprocess.run([driver, what], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.splitlines()[-1:] == ["ok"], r.stdout[-4000:]
