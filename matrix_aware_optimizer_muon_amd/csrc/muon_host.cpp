@@ -21,6 +21,7 @@
 #include <cstdio>
 #include <cstring>
 #include <exception>
+#include <memory>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -863,6 +864,18 @@ struct muon_handle_s {
   uint64_t rounding_seed = 0;
   int static_device = -1;        // muon_init_static: the GPU whose scratch array holds the workspace
   uint64_t static_generation = 0;  // ... and which of its static inits this handle is
+
+  muon_handle_s() = default;
+  muon_handle_s(const muon_handle_s&) = delete;
+  muon_handle_s& operator=(const muon_handle_s&) = delete;
+  ~muon_handle_s() {
+    for (hipStream_t ls : lane_streams) (void)hipStreamDestroy(ls);
+    if (aux_stream) (void)hipStreamDestroy(aux_stream);
+    for (hipEvent_t ej : ev_joins) (void)hipEventDestroy(ej);
+    for (hipEvent_t ev : {ev_aux, ev_adam, ev_fork})
+      if (ev) (void)hipEventDestroy(ev);
+    for (hipEvent_t ev : events) (void)hipEventDestroy(ev);
+  }
 };
 
 namespace {
@@ -1197,6 +1210,25 @@ muon_status_t static_scratch(int* dev_out, void** ptr_out) {
   return MUON_OK;
 }
 
+// Names of the handle's launches in their order, but for the gradient norm's.
+void name_phases(muon_handle_t h) {
+  if (!h->plan.apply.empty()) h->phase_names.push_back("precond_apply");
+  if (h->plan.has_adam()) h->phase_names.push_back("adamw");
+  for (const Group& g : h->plan.groups) {
+    if (g.units.empty()) continue;
+    const std::string dt = std::string(g.f32 ? "/f32" : "/bf16") + (g.lane ? "@" + std::to_string(g.lane + 1) : "");
+    h->phase_names.push_back("momentum" + dt);
+    for (int it = 0; it < h->hp.ns_steps; ++it)
+      for (int ph = 0; ph < 3; ++ph)
+        for (int tc : kLaunchOrder) {
+          if (g.gemm[ph][tc].empty()) continue;
+          h->phase_names.push_back(std::string(kPhaseNames[ph]) + dt + tile_tag(g.f32, tc) + "#" +
+                                   std::to_string(it + 1));
+        }
+    if (h->hp.ns_steps == 0) h->phase_names.push_back("update" + dt);
+  }
+}
+
 // Body shared by muon_init and muon_init_static: `plan` is built and checked
 // against the workspace already.  With `with_streams` false the handle
 // creates no streams or events: every launch of muon_step then runs on the
@@ -1206,8 +1238,8 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   std::string who;
   if (overlaps_tensors(workspace, plan.total, tensors, size_t(n_tensors), &who))
     return fail(MUON_ERR_ALIASING, who + " overlaps the workspace");
-  muon_handle_s* h = new (std::nothrow) muon_handle_s();
-  if (!h) return fail(MUON_ERR_UNSUPPORTED, "host allocation failed");
+  // everything the host holds comes first: from the streams on nothing here allocates
+  std::unique_ptr<muon_handle_s> h(new muon_handle_s());
   h->plan = std::move(plan);
   h->hp = *hp;
   h->tensors.assign(tensors, tensors + n_tensors);
@@ -1217,21 +1249,22 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   std::sort(h->spans.begin(), h->spans.end());
   h->ws = static_cast<uint8_t*>(workspace);
   h->meta = build_meta(h->plan, tensors, h->ws);
+  name_phases(h.get());
+  int max_lane = 0;
+  for (const Group& g : h->plan.groups) max_lane = std::max(max_lane, g.lane);
+  const bool aux = with_streams && h->plan.has_adam() && !h->plan.units.empty();
+  if (!with_streams) max_lane = 0;
+  h->lane_streams.reserve(size_t(max_lane));
+  h->ev_joins.reserve(size_t(max_lane));
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipMemsetAsync(h->ws, 0, h->plan.total, s);
   if (e == hipSuccess) e = hipMemcpyAsync(h->ws, h->meta.data(), h->meta.size(), hipMemcpyHostToDevice, s);
   for (const SlotPlan& sp : h->plan.slots)   // S^-1 = I until the slot's first refresh
     if (e == hipSuccess) e = launch_identity(reinterpret_cast<uint16_t*>(h->ws + sp.off_sinv), sp.dp, sp.nblocks, s);
   if (e == hipSuccess) e = hipStreamSynchronize(s);  // the host copy of meta may be reused after init
-  if (e != hipSuccess) {
-    delete h;
-    return fail(MUON_ERR_HIP, std::string("workspace initialisation: ") + hipGetErrorString(e));
-  }
+  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("workspace initialisation: ") + hipGetErrorString(e));
   h->last_stream = s;
-  int max_lane = 0;
-  for (const Group& g : h->plan.groups) max_lane = std::max(max_lane, g.lane);
-  const bool aux = with_streams && h->plan.has_adam() && !h->plan.units.empty();
-  if (with_streams && (max_lane > 0 || aux)) {
+  if (max_lane > 0 || aux) {
     e = hipEventCreateWithFlags(&h->ev_fork, hipEventDisableTiming);
     if (aux && e == hipSuccess) e = hipStreamCreateWithFlags(&h->aux_stream, hipStreamNonBlocking);
     if (aux && e == hipSuccess) e = hipEventCreateWithFlags(&h->ev_aux, hipEventDisableTiming);
@@ -1244,33 +1277,9 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
       if (e == hipSuccess) e = hipEventCreateWithFlags(&ej, hipEventDisableTiming);
       if (e == hipSuccess) h->ev_joins.push_back(ej);
     }
-    if (e != hipSuccess) {
-      if (h->ev_fork) (void)hipEventDestroy(h->ev_fork);
-      if (h->ev_aux) (void)hipEventDestroy(h->ev_aux);
-      if (h->ev_adam) (void)hipEventDestroy(h->ev_adam);
-      if (h->aux_stream) (void)hipStreamDestroy(h->aux_stream);
-      for (hipEvent_t ej : h->ev_joins) (void)hipEventDestroy(ej);
-      for (hipStream_t ls : h->lane_streams) (void)hipStreamDestroy(ls);
-      delete h;
-      return fail(MUON_ERR_HIP, std::string("lane streams: ") + hipGetErrorString(e));
-    }
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("lane streams: ") + hipGetErrorString(e));
   }
-  if (!h->plan.apply.empty()) h->phase_names.push_back("precond_apply");
-  if (h->plan.has_adam()) h->phase_names.push_back("adamw");
-  for (const Group& g : h->plan.groups) {
-    if (g.units.empty()) continue;
-    const std::string dt = std::string(g.f32 ? "/f32" : "/bf16") + (g.lane ? "@" + std::to_string(g.lane + 1) : "");
-    h->phase_names.push_back("momentum" + dt);
-    for (int it = 0; it < hp->ns_steps; ++it)
-      for (int ph = 0; ph < 3; ++ph)
-        for (int tc : kLaunchOrder) {
-          if (g.gemm[ph][tc].empty()) continue;
-          h->phase_names.push_back(std::string(kPhaseNames[ph]) + dt + tile_tag(g.f32, tc) + "#" +
-                                   std::to_string(it + 1));
-        }
-    if (hp->ns_steps == 0) h->phase_names.push_back("update" + dt);
-  }
-  *out = h;
+  *out = h.release();
   return MUON_OK;
 }
 
@@ -1599,18 +1608,11 @@ muon_status_t muon_destroy(muon_handle_t h) {
   for (hipStream_t ls : h->lane_streams) {
     const hipError_t e2 = hipStreamSynchronize(ls);
     if (e == hipSuccess) e = e2;
-    (void)hipStreamDestroy(ls);
   }
   if (h->aux_stream) {
     const hipError_t e2 = hipStreamSynchronize(h->aux_stream);
     if (e == hipSuccess) e = e2;
-    (void)hipStreamDestroy(h->aux_stream);
   }
-  for (hipEvent_t ej : h->ev_joins) (void)hipEventDestroy(ej);
-  if (h->ev_aux) (void)hipEventDestroy(h->ev_aux);
-  if (h->ev_adam) (void)hipEventDestroy(h->ev_adam);
-  if (h->ev_fork) (void)hipEventDestroy(h->ev_fork);
-  for (hipEvent_t ev : h->events) (void)hipEventDestroy(ev);
   delete h;
   if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("destroy: ") + hipGetErrorString(e));
   return MUON_OK;

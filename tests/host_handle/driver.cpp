@@ -59,6 +59,7 @@ hipError_t hipEventRecord(hipEvent_t, hipStream_t) { return hipSuccess; }
 hipError_t hipEventSynchronize(hipEvent_t) { return hipSuccess; }
 hipError_t hipEventElapsedTime(float* ms, hipEvent_t, hipEvent_t) { return *ms = 1.f, hipSuccess; }
 hipError_t hipStreamWaitEvent(hipStream_t, hipEvent_t, unsigned int) { return hipSuccess; }
+const char* hipGetErrorString(hipError_t) { return "stand-in"; }
 int roctxRangePushA(const char*) { return 0; }
 int roctxRangePop() { return 0; }
 }
