@@ -34,7 +34,8 @@
  *   muon_init() (and muon_precond_refresh()).  muon_step() only enqueues
  *   work on the given stream: it never synchronises, never allocates, and
  *   returns MUON_ERR_HIP only if a launch fails.  Nothing aborts or throws
- *   across the ABI.  A human-readable detail of the last error on the
+ *   across the ABI: where the host runs out of memory, in any call, it returns
+ *   MUON_ERR_UNSUPPORTED ("out of memory").  A human-readable detail of the last error on the
  *   calling thread is available from muon_last_error().  Non-finite values
  *   propagate as in the plain arithmetic and set bit 0 of the flags word.
  *

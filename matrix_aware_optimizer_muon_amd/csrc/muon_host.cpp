@@ -1414,83 +1414,92 @@ muon_status_t check_acts(const SlotPlan& sp, const void* acts, int64_t n_rows, i
 
 muon_status_t muon_precond_accumulate(muon_handle_t h, int32_t slot, int32_t block, const void* acts,
                                       int64_t n_rows, int64_t ld, int32_t dtype, float beta, void* stream) {
-  muon_status_t st = check_slot_block(h, slot, block);
-  if (st != MUON_OK) return st;
-  const SlotPlan& sp = h->plan.slots[size_t(slot)];
-  if ((st = check_acts(sp, acts, n_rows, ld, dtype)) != MUON_OK) return st;
-  if (!(beta >= 0.f && beta <= 1.f)) return fail(MUON_ERR_BAD_ARG, "beta must be in [0, 1]");
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  Range r("muon.precond_accumulate");
-  hipError_t e = launch_precond_accumulate(block_dev(h, sp, block), acts, n_rows, ld, dtype == MUON_F32, beta, s);
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond accumulate launch: ") + hipGetErrorString(e));
-  h->last_stream = s;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    const SlotPlan& sp = h->plan.slots[size_t(slot)];
+    if ((st = check_acts(sp, acts, n_rows, ld, dtype)) != MUON_OK) return st;
+    if (!(beta >= 0.f && beta <= 1.f)) return fail(MUON_ERR_BAD_ARG, "beta must be in [0, 1]");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Range r("muon.precond_accumulate");
+    hipError_t e = launch_precond_accumulate(block_dev(h, sp, block), acts, n_rows, ld, dtype == MUON_F32, beta, s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond accumulate launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_precond_refresh_accumulated(muon_handle_t h, int32_t slot, int32_t block, float damping,
                                                int32_t reset, void* stream) {
-  muon_status_t st = check_slot_block(h, slot, block);
-  if (st != MUON_OK) return st;
-  if (!std::isfinite(damping) || damping < 0.f) return fail(MUON_ERR_BAD_ARG, "damping must be finite and >= 0");
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  Range r("muon.precond_refresh_accumulated");
-  hipError_t e = launch_precond_refresh_accumulated(block_dev(h, h->plan.slots[size_t(slot)], block), damping,
-                                                    reset != 0,
-                                                    reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond refresh launch: ") + hipGetErrorString(e));
-  h->last_stream = s;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    if (!std::isfinite(damping) || damping < 0.f) return fail(MUON_ERR_BAD_ARG, "damping must be finite and >= 0");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Range r("muon.precond_refresh_accumulated");
+    hipError_t e = launch_precond_refresh_accumulated(block_dev(h, h->plan.slots[size_t(slot)], block), damping,
+                                                      reset != 0,
+                                                      reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond refresh launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_precond_refresh(muon_handle_t h, int32_t slot, int32_t block, const void* acts, int64_t n_rows,
                                    int64_t ld, int32_t dtype, float damping, void* stream) {
-  muon_status_t st = check_slot_block(h, slot, block);
-  if (st != MUON_OK) return st;
-  const SlotPlan& sp = h->plan.slots[size_t(slot)];
-  if ((st = check_acts(sp, acts, n_rows, ld, dtype)) != MUON_OK) return st;
-  if (!std::isfinite(damping) || damping < 0.f) return fail(MUON_ERR_BAD_ARG, "damping must be finite and >= 0");
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  Range r("muon.precond_refresh");
-  hipError_t e = launch_precond_refresh(block_dev(h, sp, block), acts, n_rows, ld, dtype == MUON_F32, damping,
-                                        reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond refresh launch: ") + hipGetErrorString(e));
-  h->last_stream = s;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    const SlotPlan& sp = h->plan.slots[size_t(slot)];
+    if ((st = check_acts(sp, acts, n_rows, ld, dtype)) != MUON_OK) return st;
+    if (!std::isfinite(damping) || damping < 0.f) return fail(MUON_ERR_BAD_ARG, "damping must be finite and >= 0");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Range r("muon.precond_refresh");
+    hipError_t e = launch_precond_refresh(block_dev(h, sp, block), acts, n_rows, ld, dtype == MUON_F32, damping,
+                                          reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond refresh launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_step(muon_handle_t h, float lr, void* stream) {
-  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
-  if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
-  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  return enqueue_step(h, lr < 0.f ? h->hp.lr : lr, static_cast<hipStream_t>(stream), nullptr);
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+    return enqueue_step(h, lr < 0.f ? h->hp.lr : lr, static_cast<hipStream_t>(stream), nullptr);
+  });
 }
 
 muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream, float* phase_ms, int32_t max_phases,
                               int32_t* n_phases) {
-  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
-  if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
-  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  const size_t np = size_t(norm_phases(h)) + h->phase_names.size();
-  if (h->events.size() < np + 1) {
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+    const size_t np = size_t(norm_phases(h)) + h->phase_names.size();
+    h->events.reserve(np + 1);
     while (h->events.size() < np + 1) {
       hipEvent_t ev;
       if (hipEventCreate(&ev) != hipSuccess) return fail(MUON_ERR_HIP, "hipEventCreate failed");
       h->events.push_back(ev);
     }
-  }
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  muon_status_t st = enqueue_step(h, lr < 0.f ? h->hp.lr : lr, s, &h->events);
-  if (st != MUON_OK) return st;
-  if (hipEventSynchronize(h->events[np]) != hipSuccess) return fail(MUON_ERR_HIP, "hipEventSynchronize failed");
-  const size_t k = std::min<size_t>(np, max_phases > 0 ? size_t(max_phases) : 0);
-  for (size_t i = 0; i < k; ++i) {
-    float ms = 0.f;
-    if (hipEventElapsedTime(&ms, h->events[i], h->events[i + 1]) != hipSuccess)
-      return fail(MUON_ERR_HIP, "hipEventElapsedTime failed");
-    if (phase_ms) phase_ms[i] = ms;
-  }
-  if (n_phases) *n_phases = int32_t(np);
-  return MUON_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    muon_status_t st = enqueue_step(h, lr < 0.f ? h->hp.lr : lr, s, &h->events);
+    if (st != MUON_OK) return st;
+    if (hipEventSynchronize(h->events[np]) != hipSuccess) return fail(MUON_ERR_HIP, "hipEventSynchronize failed");
+    const size_t k = std::min<size_t>(np, max_phases > 0 ? size_t(max_phases) : 0);
+    for (size_t i = 0; i < k; ++i) {
+      float ms = 0.f;
+      if (hipEventElapsedTime(&ms, h->events[i], h->events[i + 1]) != hipSuccess)
+        return fail(MUON_ERR_HIP, "hipEventElapsedTime failed");
+      if (phase_ms) phase_ms[i] = ms;
+    }
+    if (n_phases) *n_phases = int32_t(np);
+    return MUON_OK;
+  });
 }
 
 const char* muon_phase_name(muon_handle_t h, int32_t phase) {
@@ -1501,35 +1510,41 @@ const char* muon_phase_name(muon_handle_t h, int32_t phase) {
 }
 
 muon_status_t muon_set_adam_step(muon_handle_t h, int64_t steps_taken, void* stream) {
-  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
-  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  if (steps_taken < 0 || steps_taken > int64_t(UINT32_MAX) - 1) return fail(MUON_ERR_BAD_ARG, "step count out of range");
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = launch_adam_set(reinterpret_cast<AdamState*>(h->ws + h->plan.off_adam_state),
-                                 uint32_t(steps_taken), s);
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step set: ") + hipGetErrorString(e));
-  h->last_stream = s;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+    if (steps_taken < 0 || steps_taken > int64_t(UINT32_MAX) - 1) return fail(MUON_ERR_BAD_ARG, "step count out of range");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = launch_adam_set(reinterpret_cast<AdamState*>(h->ws + h->plan.off_adam_state),
+                                   uint32_t(steps_taken), s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step set: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_get_adam_step(muon_handle_t h, void* stream, int64_t* steps_taken) {
-  if (!h || !steps_taken) return fail(MUON_ERR_NULL_ARG, "handle or output is NULL");
-  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  AdamState st;
-  hipError_t e = hipMemcpyAsync(&st, h->ws + h->plan.off_adam_state, sizeof(st), hipMemcpyDeviceToHost, s);
-  if (e == hipSuccess) e = hipStreamSynchronize(s);
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step read: ") + hipGetErrorString(e));
-  *steps_taken = int64_t(st.t);
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!h || !steps_taken) return fail(MUON_ERR_NULL_ARG, "handle or output is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    AdamState st;
+    hipError_t e = hipMemcpyAsync(&st, h->ws + h->plan.off_adam_state, sizeof(st), hipMemcpyDeviceToHost, s);
+    if (e == hipSuccess) e = hipStreamSynchronize(s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step read: ") + hipGetErrorString(e));
+    *steps_taken = int64_t(st.t);
+    return MUON_OK;
+  });
 }
 
 size_t muon_packed_moment_bytes(int64_t n) { return n > 0 && n <= kPackMaxElems ? size_t(packed_bytes(n)) : 0; }
 
 muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed) {
-  if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
-  h->rounding_seed = seed;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    h->rounding_seed = seed;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* norm_out) {
@@ -1587,35 +1602,39 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
 }
 
 muon_status_t muon_get_flags(muon_handle_t h, void* stream, int32_t reset, uint32_t* flags) {
-  if (!h || !flags) return fail(MUON_ERR_NULL_ARG, "handle or flags is NULL");
-  if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  uint32_t v = 0;
-  hipError_t e = hipStreamSynchronize(s);
-  if (e == hipSuccess) e = hipMemcpy(&v, h->ws + h->plan.off_flags, sizeof(v), hipMemcpyDeviceToHost);
-  if (e == hipSuccess && reset) {
-    e = hipMemsetAsync(h->ws + h->plan.off_flags, 0, sizeof(uint32_t), s);
-    if (e == hipSuccess) e = hipStreamSynchronize(s);
-  }
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("flags: ") + hipGetErrorString(e));
-  *flags = v;
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!h || !flags) return fail(MUON_ERR_NULL_ARG, "handle or flags is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    uint32_t v = 0;
+    hipError_t e = hipStreamSynchronize(s);
+    if (e == hipSuccess) e = hipMemcpy(&v, h->ws + h->plan.off_flags, sizeof(v), hipMemcpyDeviceToHost);
+    if (e == hipSuccess && reset) {
+      e = hipMemsetAsync(h->ws + h->plan.off_flags, 0, sizeof(uint32_t), s);
+      if (e == hipSuccess) e = hipStreamSynchronize(s);
+    }
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("flags: ") + hipGetErrorString(e));
+    *flags = v;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_destroy(muon_handle_t h) {
-  if (!h) return MUON_OK;
-  hipError_t e = hipStreamSynchronize(h->last_stream);
-  for (hipStream_t ls : h->lane_streams) {
-    const hipError_t e2 = hipStreamSynchronize(ls);
-    if (e == hipSuccess) e = e2;
-  }
-  if (h->aux_stream) {
-    const hipError_t e2 = hipStreamSynchronize(h->aux_stream);
-    if (e == hipSuccess) e = e2;
-  }
-  delete h;
-  if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("destroy: ") + hipGetErrorString(e));
-  return MUON_OK;
+  return guarded([&]() -> muon_status_t {
+    if (!h) return MUON_OK;
+    hipError_t e = hipStreamSynchronize(h->last_stream);
+    for (hipStream_t ls : h->lane_streams) {
+      const hipError_t e2 = hipStreamSynchronize(ls);
+      if (e == hipSuccess) e = e2;
+    }
+    if (h->aux_stream) {
+      const hipError_t e2 = hipStreamSynchronize(h->aux_stream);
+      if (e == hipSuccess) e = e2;
+    }
+    delete h;
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("destroy: ") + hipGetErrorString(e));
+    return MUON_OK;
+  });
 }
 
 const char* muon_status_str(muon_status_t s) {
