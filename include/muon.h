@@ -35,9 +35,10 @@
  *   work on the given stream: it never synchronises, never allocates, and
  *   returns MUON_ERR_HIP only if a launch fails.  Nothing aborts or throws
  *   across the ABI: where the host runs out of memory, in any call, it returns
- *   MUON_ERR_UNSUPPORTED ("out of memory").  A human-readable detail of the last error on the
- *   calling thread is available from muon_last_error().  Non-finite values
- *   propagate as in the plain arithmetic and set bit 0 of the flags word.
+ *   MUON_ERR_UNSUPPORTED ("out of memory").  A human-readable detail of the
+ *   last error on the calling thread is available from muon_last_error().
+ *   Non-finite values propagate as in the plain arithmetic and set bit 0 of the
+ *   flags word.
  *
  * Threading: one handle may be used by one stream at a time.
  * Streams: `stream` arguments are hipStream_t values passed as void*;
@@ -120,6 +121,9 @@ typedef struct {
                            cols); receives the orthogonalised update O of this
                            step, before lr/scale.  NULL = not written.        */
   int32_t kind;         /* muon_kind_t; 0 (MUON) in a zero-filled struct      */
+#ifdef __GNUC__
+  __extension__         /* an unnamed union, in C before C11 too */
+#endif
   union {
     int32_t state_bits; /* kind ADAMW: bits a moment's element is held in: 0 or
                            32 float32, 8 packed (see "Packed moments" below);
