@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamDev* __restri
   const AdamDev& d = tensors[tk.tensor];
   const float lr = p.lr * d.lr_mult;
   const float factor = p.factor ? gld<float>(p.factor) : 1.f;
-  const float inv_bc1 = p.state->inv_bc1, inv_sqrt_bc2 = p.state->inv_sqrt_bc2;
+  const float inv_bc1 = p.state->now.inv_bc1, inv_sqrt_bc2 = p.state->now.inv_sqrt_bc2;
   const int64_t j0 = tk.c0 + int64_t(threadIdx.x) * 8;
   if (j0 >= d.len) return;
   if (d.f32) adamw_segment<true>(d, tk, p, lr, factor, inv_bc1, inv_sqrt_bc2, j0);

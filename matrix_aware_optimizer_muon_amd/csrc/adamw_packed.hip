@@ -490,35 +490,39 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
 // units are busy for about 100 of the 128 us (42 instructions an element), so
 // the root and the reciprocal are the hardware's: with the language's, 65
 // instructions an element, the same took 151 us, all of them.
-// BEGINS: no launch has advanced the step count before this one.  Every wave
-// takes the next step's bias corrections itself, while its loads are under
-// way, and the last block advances the count (launch_adamw_packed).
+// BEGINS: no launch has advanced the step count before this one.  Its waves
+// take the next step's count and corrections; the last block that is done
+// advances the count, and a block before the others takes the corrections of
+// the step after (launch_adamw_packed).
 template <bool F32, bool PRECISE, bool ROWS, bool BEGINS>
-__global__ __launch_bounds__(kThreads, BEGINS ? 4 : 8) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
-                                                                                const PackedTask* __restrict__ tasks,
-                                                                                PackedParams p) {
-  const PackedTask tk = tasks[blockIdx.x];
-  const PackedDev d = load_desc(tensors + tk.tensor);
+__global__ __launch_bounds__(kThreads, 8) void adamw_packed_kernel(const PackedDev* __restrict__ tensors,
+                                                                   const PackedTask* __restrict__ tasks,
+                                                                   PackedParams p) {
   const uint32_t t = sreg_i32(gld<uint32_t>(&p.adam.state->t)) + BEGINS;
-  const auto begin = [&](const PackedDev& d, const PackedParams& p) {
-    const uint32_t key = tensor_key(p.seed, t, d.tensor);
-    if constexpr (BEGINS) return StepScalars(d, p, adam_bias_short(t, p.adam.beta1, p.adam.beta2), key);
-    else return StepScalars(d, p, {p.adam.state->inv_bc1, p.adam.state->inv_sqrt_bc2}, key);
-  };
-  bool bad;
-  if constexpr (ROWS) {
-    bad = step_rows_chunk<F32, PRECISE>(d, p, begin, tk.c0);
-  } else {
-    const int64_t left = d.n - tk.c0;
-    if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, begin, tk.c0);
-    else bad = step_last_chunk<F32, PRECISE>(d, p, begin, tk.c0, static_cast<uint32_t>(left));
+  const uint32_t before = BEGINS && p.advance != nullptr;    // blocks before the tasks'
+  if (blockIdx.x >= before) {
+    const PackedTask tk = tasks[blockIdx.x - before];
+    const PackedDev d = load_desc(tensors + tk.tensor);
+    const auto begin = [&](const PackedDev& d, const PackedParams& p) {
+      const AdamState& st = *p.adam.state;
+      return StepScalars(d, p, BEGINS ? st.next[t & 1] : st.now, tensor_key(p.seed, t, d.tensor));
+    };
+    bool bad;
+    if constexpr (ROWS) {
+      bad = step_rows_chunk<F32, PRECISE>(d, p, begin, tk.c0);
+    } else {
+      const int64_t left = d.n - tk.c0;
+      if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, begin, tk.c0);
+      else bad = step_last_chunk<F32, PRECISE>(d, p, begin, tk.c0, static_cast<uint32_t>(left));
+    }
+    if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(p.adam.flags, 1u);
+  } else if (threadIdx.x == 0) {
+    adam_prepare(p.advance, t + 1, p.adam.beta1, p.adam.beta2);    // in the place that no wave of step t reads
   }
-  if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(p.adam.flags, 1u);
   if constexpr (BEGINS) {
     if (p.advance == nullptr) return;          // a launch after this one advances it
-    __syncthreads();                           // every wave has read the count
-    if (threadIdx.x == 0 && arrive_last(p.arrivals))
-      adam_store(p.advance, t, adam_bias_short(t, p.adam.beta1, p.adam.beta2));
+    __syncthreads();                           // every wave has read the count and its corrections
+    if (threadIdx.x == 0 && arrive_last(p.arrivals)) p.advance->t = t;
   }
 }
 
@@ -633,7 +637,7 @@ const PackedTask* launch_step(bool precise, bool begins, const PackedDev* tensor
                                           : adamw_packed_kernel<F32, true, ROWS, false>)
                                 : (begins ? adamw_packed_kernel<F32, false, ROWS, true>
                                           : adamw_packed_kernel<F32, false, ROWS, false>);
-    kernel<<<n, kThreads, 0, s>>>(tensors, tasks, p);
+    kernel<<<n + (p.advance != nullptr), kThreads, 0, s>>>(tensors, tasks, p);
   }
   return tasks + n;
 }

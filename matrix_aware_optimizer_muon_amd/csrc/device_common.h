@@ -278,39 +278,25 @@ __device__ __forceinline__ void update_w8_loaded(const UnitDev& u, int i, int j0
 namespace muon {
 
 // Bias corrections of AdamW's step t.
-struct AdamBias { float inv_bc1, inv_sqrt_bc2; };
 __device__ __forceinline__ AdamBias adam_bias(uint32_t t, float beta1, float beta2) {
   const double bc1 = 1.0 - pow(double(beta1), double(t));
   const double bc2 = 1.0 - pow(double(beta2), double(t));
   return {float(1.0 / bc1), float(1.0 / sqrt(bc2))};
 }
 
-// The same by repeated squaring, for kernels in which every wave takes them:
-// some 20 dependent products instead of two calls of pow (which took 1.2 us of
-// a launch of 6.6 us).  Each power is off by t units of 2^-53, so its float32 result is the
-// same but where the exact one lies that close to a rounding border.
-__device__ __forceinline__ AdamBias adam_bias_short(uint32_t t, float beta1, float beta2) {
-  double p1 = 1.0, p2 = 1.0, b1 = beta1, b2 = beta2;
-  for (; t; t >>= 1) {
-    if (t & 1) {
-      p1 *= b1;
-      p2 *= b2;
-    }
-    b1 *= b1;
-    b2 *= b2;
-  }
-  return {float(1.0 / (1.0 - p1)), float(1.0 / sqrt(1.0 - p2))};
+// The corrections of a step are taken while the one before it runs, so that
+// whichever launch advances the count (its own, the gradient norm's, the
+// packed tensors') takes them from one place.
+__device__ __forceinline__ void adam_prepare(AdamState* st, uint32_t t, float beta1, float beta2) {
+  st->next[t & 1] = adam_bias(t, beta1, beta2);
 }
 
-// Next step of the AdamW count: t and the bias corrections of that step.
-__device__ __forceinline__ void adam_store(AdamState* st, uint32_t t, const AdamBias& b) {
-  st->t = t;
-  st->inv_bc1 = b.inv_bc1;
-  st->inv_sqrt_bc2 = b.inv_sqrt_bc2;
-}
+// Next step of the AdamW count.
 __device__ __forceinline__ void adam_advance(AdamState* st, float beta1, float beta2) {
   const uint32_t t = st->t + 1;
-  adam_store(st, t, adam_bias(t, beta1, beta2));
+  st->t = t;
+  st->now = st->next[t & 1];
+  adam_prepare(st, t + 1, beta1, beta2);
 }
 
 // Called by one thread of every block of a launch: true in the one that comes

@@ -1210,6 +1210,14 @@ muon_status_t static_scratch(int* dev_out, void** ptr_out) {
   return MUON_OK;
 }
 
+// The AdamW count at `steps` taken: one less, advanced as a step does it,
+// which also takes the next step's corrections.
+hipError_t set_adam_count(muon_handle_t h, uint32_t steps, hipStream_t s) {
+  AdamState* const st = reinterpret_cast<AdamState*>(h->ws + h->plan.off_adam_state);
+  const hipError_t e = launch_adam_set(st, steps - 1u, s);
+  return e == hipSuccess ? launch_adam_tick(st, h->hp.adam_beta1, h->hp.adam_beta2, s) : e;
+}
+
 // Names of the handle's launches in their order, but for the gradient norm's.
 void name_phases(muon_handle_t h) {
   if (!h->plan.apply.empty()) h->phase_names.push_back("precond_apply");
@@ -1261,6 +1269,7 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   if (e == hipSuccess) e = hipMemcpyAsync(h->ws, h->meta.data(), h->meta.size(), hipMemcpyHostToDevice, s);
   for (const SlotPlan& sp : h->plan.slots)   // S^-1 = I until the slot's first refresh
     if (e == hipSuccess) e = launch_identity(reinterpret_cast<uint16_t*>(h->ws + sp.off_sinv), sp.dp, sp.nblocks, s);
+  if (e == hipSuccess && h->plan.has_adam()) e = set_adam_count(h.get(), 0, s);
   if (e == hipSuccess) e = hipStreamSynchronize(s);  // the host copy of meta may be reused after init
   if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("workspace initialisation: ") + hipGetErrorString(e));
   h->last_stream = s;
@@ -1515,8 +1524,7 @@ muon_status_t muon_set_adam_step(muon_handle_t h, int64_t steps_taken, void* str
     if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
     if (steps_taken < 0 || steps_taken > int64_t(UINT32_MAX) - 1) return fail(MUON_ERR_BAD_ARG, "step count out of range");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = launch_adam_set(reinterpret_cast<AdamState*>(h->ws + h->plan.off_adam_state),
-                                   uint32_t(steps_taken), s);
+    hipError_t e = set_adam_count(h, uint32_t(steps_taken), s);
     if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("adam step set: ") + hipGetErrorString(e));
     h->last_stream = s;
     return MUON_OK;

@@ -173,11 +173,11 @@ struct AdamDev {
 };
 constexpr int kAdamChunk = 2048;       // elements of one row per block (256 threads x 8)
 struct AdamTask { int32_t tensor, row; int64_t c0; };
+struct AdamBias { float inv_bc1, inv_sqrt_bc2; };   // of step t: 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
 struct AdamState {                     // on the device, in the workspace
   uint32_t t;                          // steps taken
-  float inv_bc1;                       // 1 / (1 - b1^t)
-  float inv_sqrt_bc2;                  // 1 / sqrt(1 - b2^t)
-  uint32_t pad;
+  AdamBias now;                        // of step t, where a launch of its own or the norm's has advanced the count
+  AdamBias next[2];                    // of step t + 1, at (t + 1) & 1
 };
 struct AdamParams {
   float lr, beta1, beta2, eps, weight_decay;
@@ -283,11 +283,11 @@ hipError_t launch_adamw(const AdamDev* tensors, const AdamTask* tasks, int n_tas
 // n: chunks of each kind of tensor, in the order of the tasks: bf16 without
 // and with gaps between rows, float32 without and with
 constexpr int kPackKinds = 4;
-// begins: no launch has advanced the step count; the last of these does.  For
-// at most kPackBeginMost chunks: a launch less, but every wave then takes the
-// bias corrections, in float64.  Steps of one tensor, with a count launched
-// before and without: 1 M bf16 elements 7.9 and 5.9 us, 4 M (2048 chunks) 12.2
-// and 11.3 us, 82 M 134 and 171 us.
+// begins: no launch has advanced the step count; the last of these does, with
+// a block more.  For at most kPackBeginMost chunks: a launch less, but every
+// block then reports its end.  Steps of one bf16 tensor from a graph, with a
+// count launched before and without: 38 K elements 6.2 and 4.9 us, 1 M 7.3 and
+// 5.9, 4 M (2048 chunks) 11.4 and 10.3, 8 M 16.7 and 16.8, 82 M 128.0 and 129.0.
 constexpr int kPackBeginMost = 2048;
 MUON_WEAK hipError_t launch_adamw_packed(const PackedDev* tensors, const PackedTask* tasks, const int* n, bool begins,
                                          PackedParams p, hipStream_t s);
