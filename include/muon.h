@@ -43,6 +43,8 @@
  * Threading: one handle may be used by one stream at a time.
  * Streams: `stream` arguments are hipStream_t values passed as void*;
  *   NULL means the default stream.
+ * Devices: a handle's buffers lie on one GPU, which has to be the calling
+ *   thread's current device in every call.
  */
 #ifndef MUON_H
 #define MUON_H

@@ -402,10 +402,10 @@ class MuonStep:
         return ctypes.c_void_p(self._torch_stream(stream).cuda_stream)
 
     def _launch(self, function, *args):
-        """Call a library function that launches kernels, with the handle's
-        device the current one (HIP launches on that)."""
+        """Call a library function with the handle's device the current one:
+        HIP launches on that, and the default stream is that one's."""
         cuda = _torch().cuda
-        if cuda.current_device() == self.device.index:
+        if self.device.index is None or cuda.current_device() == self.device.index:
             status = function(*args)
         else:
             with cuda.device(self.device):
@@ -441,8 +441,8 @@ class MuonStep:
         cap = 4096
         ms = (ctypes.c_float * cap)()
         n = ctypes.c_int32(0)
-        self._check(self._lib.muon_step_timed(self._h, ctypes.c_float(lr), self._stream(stream), ms, cap,
-                                         ctypes.byref(n)))
+        self._launch(self._lib.muon_step_timed, self._h, ctypes.c_float(lr), self._stream(stream), ms, cap,
+                     ctypes.byref(n))
         return [(self._lib.muon_phase_name(self._h, i).decode(), ms[i]) for i in range(min(n.value, cap))]
 
     def precond_refresh(self, slot: int, block: int, acts, damping: float = 1e-4, stream=None):
@@ -453,9 +453,8 @@ class MuonStep:
         if dt is None:
             raise ValueError(f"unsupported activation dtype {acts.dtype}")
         s = self._torch_stream(stream)
-        self._check(self._lib.muon_precond_refresh(self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
-                                              acts.shape[0], acts.stride(0), dt, ctypes.c_float(damping),
-                                              ctypes.c_void_p(s.cuda_stream)))
+        self._launch(self._lib.muon_precond_refresh, self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
+                     acts.shape[0], acts.stride(0), dt, ctypes.c_float(damping), ctypes.c_void_p(s.cuda_stream))
         self._guard(acts, s)
 
     def precond_accumulate(self, slot: int, block: int, acts, beta: float = 1.0, stream=None):
@@ -468,16 +467,15 @@ class MuonStep:
         if dt is None:
             raise ValueError(f"unsupported activation dtype {acts.dtype}")
         s = self._torch_stream(stream)
-        self._check(self._lib.muon_precond_accumulate(self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
-                                                 acts.shape[0], acts.stride(0), dt, ctypes.c_float(beta),
-                                                 ctypes.c_void_p(s.cuda_stream)))
+        self._launch(self._lib.muon_precond_accumulate, self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
+                     acts.shape[0], acts.stride(0), dt, ctypes.c_float(beta), ctypes.c_void_p(s.cuda_stream))
         self._guard(acts, s)
 
     def precond_refresh_accumulated(self, slot: int, block: int, damping: float = 1e-4, reset: bool = True,
                                     stream=None):
         """Rebuild S^-1 of (slot, block) from its running second moment."""
-        self._check(self._lib.muon_precond_refresh_accumulated(self._h, slot, block, ctypes.c_float(damping),
-                                                          int(reset), self._stream(stream)))
+        self._launch(self._lib.muon_precond_refresh_accumulated, self._h, slot, block, ctypes.c_float(damping),
+                     int(reset), self._stream(stream))
 
     def set_rounding_seed(self, seed: int):
         """Seed of the random rounding of packed moments (0 until set)."""
@@ -496,7 +494,9 @@ class MuonStep:
             raise ValueError(f"a maximum norm is 0, infinite, or a number that float32 holds as neither: {max_norm}")
         if max_norm > 0 and self._norm_out is None:
             torch = _torch()
-            if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.device(self.device):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:
                 raise RuntimeError("the norm of a static handle is set for the first time before a capture: "
                                    "its buffer must not belong to the captured graph")
             norm_out = torch.zeros(2, device=self.device)
@@ -570,22 +570,22 @@ class MuonStep:
 
     def set_adam_step(self, steps_taken: int, stream=None):
         """Resume the AdamW step count (steps already taken)."""
-        self._check(self._lib.muon_set_adam_step(self._h, int(steps_taken), self._stream(stream)))
+        self._launch(self._lib.muon_set_adam_step, self._h, int(steps_taken), self._stream(stream))
 
     def adam_step(self, stream=None) -> int:
         """AdamW steps taken so far (synchronises the stream)."""
         v = ctypes.c_int64(0)
-        self._check(self._lib.muon_get_adam_step(self._h, self._stream(stream), ctypes.byref(v)))
+        self._launch(self._lib.muon_get_adam_step, self._h, self._stream(stream), ctypes.byref(v))
         return v.value
 
     def flags(self, reset: bool = False, stream=None) -> int:
         v = ctypes.c_uint32(0)
-        self._check(self._lib.muon_get_flags(self._h, self._stream(stream), int(reset), ctypes.byref(v)))
+        self._launch(self._lib.muon_get_flags, self._h, self._stream(stream), int(reset), ctypes.byref(v))
         return v.value
 
     def close(self):
         if getattr(self, "_h", None):
-            self._check(self._lib.muon_destroy(self._h))
+            self._launch(self._lib.muon_destroy, self._h)
             self._h = None
 
     def __del__(self):

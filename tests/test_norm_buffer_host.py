@@ -1,6 +1,7 @@
 """Host-only checks of how the binding sets the gradient norm and keeps its
 buffer (no GPU): a recording stand-in for torch and for the library."""
 
+import contextlib
 import ctypes
 import types
 
@@ -19,7 +20,7 @@ class Recorder:
         stream = types.SimpleNamespace(synchronize=lambda: self.events.append("synchronize"), cuda_stream=0)
         self.cuda = types.SimpleNamespace(current_stream=lambda device=None: stream,
                                           is_current_stream_capturing=lambda: capturing,
-                                          current_device=lambda: 0)
+                                          current_device=lambda: 0, device=lambda d: contextlib.nullcontext())
 
     def zeros(self, *shape, **kw):
         self.events.append("zeros")
