@@ -295,6 +295,22 @@ __device__ __forceinline__ PackedDev chunk_desc(PackedDev d, int64_t c0) {
   return d;
 }
 
+// Debug builds: a chunk starts inside its tensor, at a multiple of its size,
+// and the tensor's blocks are those of its elements; flag bit 2 otherwise.
+__device__ __forceinline__ bool task_in_bounds(const PackedDev& d, int64_t c0, uint32_t* flags) {
+  const bool ok = c0 >= 0 && c0 < d.n && c0 % kPackChunk == 0 && d.blocks == (d.n + kPackBlock - 1) / kPackBlock &&
+                  d.cols > 0 && d.n % d.cols == 0 && d.ld_param >= d.cols && d.ld_grad >= d.cols;
+  if (!ok && threadIdx.x == 0) atomicOr(flags, kFlagBounds);
+  return ok;
+}
+
+// ... and its values lie inside the caller's.
+__device__ __forceinline__ bool values_in_bounds(const PackedDev& d, int64_t n_values, uint32_t* flags) {
+  const bool ok = d.value0 >= 0 && d.value0 + d.n <= n_values;
+  if (!ok && threadIdx.x == 0) atomicOr(flags, kFlagBounds);
+  return ok;
+}
+
 // What one step holds for all elements of a tensor.
 struct StepScalars {
   float factor, beta1, beta2, c1, c2, inv_sqrt_bc2, eps, decay, step;
@@ -507,14 +523,16 @@ __global__ __launch_bounds__(kThreads, 8) void adamw_packed_kernel(const PackedD
       const AdamState& st = *p.adam.state;
       return StepScalars(d, p, BEGINS ? st.next[t & 1] : st.now, tensor_key(p.seed, t, d.tensor));
     };
-    bool bad;
-    if constexpr (ROWS) {
-      bad = step_rows_chunk<F32, PRECISE>(d, p, begin, tk.c0);
-    } else {
-      const int64_t left = d.n - tk.c0;
-      if (left >= kPackChunk) bad = step_whole_chunk<F32, PRECISE>(d, p, begin, tk.c0);
-      else bad = step_last_chunk<F32, PRECISE>(d, p, begin, tk.c0, static_cast<uint32_t>(left));
-    }
+    const auto step = [&]() -> bool {
+      if constexpr (ROWS) {
+        return step_rows_chunk<F32, PRECISE>(d, p, begin, tk.c0);
+      } else {
+        const int64_t left = d.n - tk.c0;
+        if (left >= kPackChunk) return step_whole_chunk<F32, PRECISE>(d, p, begin, tk.c0);
+        return step_last_chunk<F32, PRECISE>(d, p, begin, tk.c0, static_cast<uint32_t>(left));
+      }
+    };
+    const bool bad = (!MUON_DEBUG_BOUNDS || task_in_bounds(d, tk.c0, p.adam.flags)) && step();
     if (__any(bad) && (threadIdx.x & 63) == 0) atomicOr(p.adam.flags, 1u);
   } else if (threadIdx.x == 0) {
     adam_prepare(p.advance, t + 1, p.adam.beta1, p.adam.beta2);    // in the place that no wave of step t reads
@@ -544,6 +562,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const PackedDev* __restr
   constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedTask tk = tasks[blockIdx.x];
   const PackedDev d = load_desc(tensors + tk.tensor);
+  if constexpr (MUON_DEBUG_BOUNDS)
+    if (!task_in_bounds(d, tk.c0, flags) || !values_in_bounds(d, n_values, flags)) return;
   const ValueRuns<F32> runs(values, n_values, d, tk.c0);
   const int64_t left = d.n - tk.c0, blocks_left = d.blocks * kPackBlock - tk.c0;
   float m[G][W], v[G][W];
@@ -588,10 +608,12 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const PackedDev* __restr
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const PackedDev* __restrict__ tensors,
                                                           const PackedTask* __restrict__ tasks, void* values,
-                                                          int64_t n_values) {
+                                                          int64_t n_values, uint32_t* flags) {
   constexpr int W = kWidth<F32>, G = kGroups<F32>;
   const PackedTask tk = tasks[blockIdx.x];
   const PackedDev d = load_desc(tensors + tk.tensor);
+  if constexpr (MUON_DEBUG_BOUNDS)
+    if (!task_in_bounds(d, tk.c0, flags) || !values_in_bounds(d, n_values, flags)) return;
   const ValueRuns<F32> runs(values, n_values, d, tk.c0);
   const PackedDev c = chunk_desc<F32>(d, tk.c0);
   const int64_t left = d.n - tk.c0;
@@ -672,10 +694,10 @@ hipError_t launch_pack_moments(const PackedDev* tensors, const PackedTask* tasks
 }
 
 hipError_t launch_unpack_moments(const PackedDev* tensors, const PackedTask* tasks, int n_tasks, void* values,
-                                 int64_t n_values, bool f32, hipStream_t s) {
+                                 int64_t n_values, bool f32, uint32_t* flags, hipStream_t s) {
   if (n_tasks <= 0) return hipSuccess;
-  if (f32) unpack_kernel<true><<<n_tasks, kThreads, 0, s>>>(tensors, tasks, values, n_values);
-  else unpack_kernel<false><<<n_tasks, kThreads, 0, s>>>(tensors, tasks, values, n_values);
+  if (f32) unpack_kernel<true><<<n_tasks, kThreads, 0, s>>>(tensors, tasks, values, n_values, flags);
+  else unpack_kernel<false><<<n_tasks, kThreads, 0, s>>>(tensors, tasks, values, n_values, flags);
   return hipGetLastError();
 }
 

@@ -136,6 +136,19 @@ __device__ __forceinline__ void finish(const NormParams& p, int blocks, double* 
   }
 }
 
+// Debug builds: a chunk is one of the tensor that the list gives it to; flag
+// bit 2 otherwise.
+__device__ __forceinline__ bool chunk_in_bounds(const NormParams& p, int64_t c, int32_t tensor) {
+  bool ok = tensor >= 0 && tensor < p.n_tensors;
+  if (ok) {
+    const NormDev& d = p.tensors[tensor];
+    ok = c >= d.chunk0 && (c - d.chunk0) * kNormChunk < d.n && d.cols > 0 && d.n % d.cols == 0 &&
+         (d.flat || d.ld >= d.cols);
+  }
+  if (!ok && threadIdx.x == 0) atomicOr(p.flags, kFlagBounds);
+  return ok;
+}
+
 // The block that is done last finishes: a launch of its own for that takes 6 us
 // and another one's gap.
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormParams p) {
@@ -143,7 +156,10 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(NormParams p) {
   __shared__ bool last;
   double sum[4] = {};
   for (int64_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    const NormDev& d = p.tensors[p.chunk_tensor[c]];
+    const int32_t tensor = p.chunk_tensor[c];
+    if constexpr (MUON_DEBUG_BOUNDS)
+      if (!chunk_in_bounds(p, c, tensor)) continue;
+    const NormDev& d = p.tensors[tensor];
     const int64_t c0 = (c - d.chunk0) * kNormChunk;
     if (d.f32) add_chunk<true>(d, c0, sum);
     else add_chunk<false>(d, c0, sum);

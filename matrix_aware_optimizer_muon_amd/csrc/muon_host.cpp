@@ -908,7 +908,8 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
                         reinterpret_cast<const int32_t*>(h->ws + plan.off_chunk_tensor), plan.norm_chunks,
                         h->max_norm,
                         reinterpret_cast<double*>(h->ws + plan.off_norm_part), ns, arrivals, h->norm_out,
-                        plan.has_adam() ? adam_state : nullptr, hp.adam_beta1, hp.adam_beta2};
+                        plan.has_adam() ? adam_state : nullptr, hp.adam_beta1, hp.adam_beta2,
+                        int32_t(h->tensors.size()), reinterpret_cast<uint32_t*>(h->ws + plan.off_flags)};
     const hipError_t e = launch_grad_norm(np, s);
     if (e != hipSuccess || !mark()) return fail(MUON_ERR_HIP, std::string("grad norm launch: ") + hipGetErrorString(e));
     factor = &ns->factor;
@@ -1602,7 +1603,8 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
     Range r("muon.unpack_moments");
     hipError_t e = launch_unpack_moments(reinterpret_cast<const PackedDev*>(h->ws + plan.off_packed_dev),
                                          reinterpret_cast<const PackedTask*>(h->ws + plan.off_packed_tasks),
-                                         int(plan.packed_tasks.size()), values, plan.packed_elems, dtype == MUON_F32, s);
+                                         int(plan.packed_tasks.size()), values, plan.packed_elems, dtype == MUON_F32,
+                                         reinterpret_cast<uint32_t*>(h->ws + plan.off_flags), s);
     if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("unpack moments launch: ") + hipGetErrorString(e));
     h->last_stream = s;
     return MUON_OK;

@@ -256,6 +256,8 @@ struct NormParams {
   float* norm_out;                     // NULL, or two floats that get norm and factor as well
   AdamState* adam;                     // NULL, or the count to advance in the same launch
   float beta1, beta2;
+  int32_t n_tensors;                   // (checked in a debug build)
+  uint32_t* flags;                     // the handle's flag word (bounds checks of a debug build)
 };
 
 hipError_t launch_momentum(bool f32, const UnitDev* units, const EwTask* tasks, int n_tasks,
@@ -296,7 +298,8 @@ MUON_WEAK hipError_t launch_pack_moments(const PackedDev* tensors, const PackedT
                                          const void* values, int64_t n_values, bool f32, uint32_t* flags,
                                          hipStream_t s);
 MUON_WEAK hipError_t launch_unpack_moments(const PackedDev* tensors, const PackedTask* tasks, int n_tasks,
-                                           void* values, int64_t n_values, bool f32, hipStream_t s);
+                                           void* values, int64_t n_values, bool f32, uint32_t* flags,
+                                           hipStream_t s);
 MUON_WEAK hipError_t launch_grad_norm(const NormParams& p, hipStream_t s);
 
 }  // namespace muon

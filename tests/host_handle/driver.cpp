@@ -92,7 +92,8 @@ hipError_t launch_pack_moments(const PackedDev*, const PackedTask*, int, const v
                                hipStream_t) {
   return g_launch;
 }
-hipError_t launch_unpack_moments(const PackedDev*, const PackedTask*, int, void*, int64_t, bool, hipStream_t) {
+hipError_t launch_unpack_moments(const PackedDev*, const PackedTask*, int, void*, int64_t, bool, uint32_t*,
+                                 hipStream_t) {
   return g_launch;
 }
 hipError_t launch_grad_norm(const NormParams&, hipStream_t) { return g_launch; }
