@@ -559,7 +559,8 @@ class MuonStep:
     def split_moments(self, values):
         """Views of `values` (pack_moments' layout) by tensor: a list of
         (first, second) pairs, each rows x cols, in the order of the packed
-        tensors."""
+        tensors.  Both ways: copying float32 moments into the views of an empty
+        [2, packed_elements()] tensor makes the values that pack_moments takes."""
         pairs, at = [], 0
         for d in self._descs[:self._n]:
             if d.kind == KIND_ADAMW and d.state_bits == 8:

@@ -276,3 +276,37 @@ def test_debug_build_matches():
         st.close()
     for a, b in zip(*states):
         assert torch.equal(a, b)
+
+
+def test_run_moves_from_float32_moments_to_packed_ones():
+    say("case: three steps with float32 moments, then packed ones from them, against the oracle")
+    hp = mm.default_hparams()
+    xs = [Packed((430, k), s, d, ld=ld) for k, (s, d, ld) in enumerate(
+        [((300, 64), "bf16", None), ((777,), "f32", None), ((37, 50), "bf16", 56)])]
+    old = [tuple(torch.zeros(x.shape, device="cuda") for _ in range(2)) for x in xs]
+    st = mm.MuonStep([mm.adam_tensor_desc(x.dW, x.dG, *mv) for x, mv in zip(xs, old)], hp)
+    for t in (1, 2, 3):
+        for x in xs:
+            x.grad(t)
+        st.step()
+    steps = st.adam_step()
+    st.close()
+    opt = mm.MuonStep([x.desc() for x in xs], hp)
+    values = torch.empty(2, opt.packed_elements(), device="cuda")
+    for (first, second), (m, v) in zip(opt.split_moments(values), old):
+        first.copy_(m.reshape(first.shape)), second.copy_(v.reshape(second.shape))
+    opt.pack_moments(values)
+    opt.set_adam_step(steps)
+    for x, (m, v) in zip(xs, old):
+        x.mem = pm.encode(m.cpu().numpy().reshape(-1), v.cpu().numpy().reshape(-1))
+        assert np.array_equal(x.dM.cpu().numpy(), x.mem[0]) and np.array_equal(x.dV.cpu().numpy(), x.mem[1])
+        x.w = from_device(torch, x.dW.contiguous(), x.dtype).reshape(x.w.shape)
+        x.ring = [b.clone() for b in x.bufs]
+    for t in (4, 5):
+        for x in xs:
+            x.grad(t)
+        opt.step()
+        for k, x in enumerate(xs):
+            x.check(t, k, hp, label=f"step {t}")
+    assert opt.flags() == 0 and opt.adam_step() == 5
+    opt.close()
