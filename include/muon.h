@@ -326,6 +326,9 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
  * min(1, max_norm / norm) as it reads it; the gradients in memory stay as they
  * are.  INFINITY measures without clipping (the factor is always 1), 0 (the
  * default) switches both off.
+ * The norm is this handle's alone: where a model's tensors are spread over
+ * several handles (over GPUs, or in one process), each would clip by the norm
+ * of its own share, with a factor of its own.
  * A gradient that is not finite makes the norm so, and with a finite max_norm
  * the factor: NaN for NaN, 0 for an infinite norm (whose infinite gradients
  * become NaN).
