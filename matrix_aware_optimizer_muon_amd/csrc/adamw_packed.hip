@@ -81,9 +81,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 }
 
 // Streaming accesses for weights, gradients, values and every store: of 82 M
-// bf16 elements a step and its unpacking took 155 + 83 us without them, 145 +
-// 73 with them.  The moments' bytes are read the ordinary way: read streaming
-// they took unpacking from 71 to 80 us and a float32 step from 93 to 100.
+// bf16 elements a step takes 129 us with them and 150 without, unpacking 72 and
+// 84.  The moments' bytes are read the ordinary way: read streaming they take
+// the step to 136 us, unpacking to 80.
 template <typename T>
 __device__ __forceinline__ T gld_nt(const void* p) {
   return __builtin_nontemporal_load((const MUON_GLOBAL T*)p);
@@ -505,7 +505,11 @@ __device__ __forceinline__ bool step_rows_chunk(const PackedDev& d, const Packed
 // in 128 us (6.4 TB/s), 38.6 M float32 ones in 93 us (6.6 TB/s).  The vector
 // units are busy for about 100 of the 128 us (42 instructions an element), so
 // the root and the reciprocal are the hardware's: with the language's, 65
-// instructions an element, the same took 151 us, all of them.
+// instructions an element, the same takes 156 us, float32 99 in place of 95.
+// Rows with gaps: 38.5 M bf16 elements in rows of 767 take 110 us (62 without
+// gaps), float32 ones 104 (94): a 64-bit division a group, the loads only after
+// it, and one element after another where a row ends in a group (71
+// instructions an element).
 // BEGINS: no launch has advanced the step count before this one.  Its waves
 // take the next step's count and corrections; the last block that is done
 // advances the count, and a block before the others takes the corrections of

@@ -9,9 +9,13 @@
 // order is fixed all the same (block b of n adds chunks b, b + n, ..., and the
 // blocks' sums are added in block order), so a step repeats bit for bit.
 //
-// HBM-bound: 2 bytes per bf16 element.  The blocks stride through the chunks
-// together: with a contiguous range each, 39 M bf16 elements took 24 us, so 19,
-// of which about 4 are the launch and the last block's sums.
+// HBM-bound: 2 bytes per bf16 element, 4 per float32 one (38.5 M of them 30
+// us, 5.2 TB/s).  The blocks stride through the chunks together: with a
+// contiguous range each, 39 M bf16 elements took 24 us, so 19, of which about 4
+// are the launch and the last block's sums.  Rows with gaps: 38.5 M elements in
+// rows of 767 take 48 to 57 us in bf16 and 48 to 66 in float32, as a thread has
+// one load in flight there, behind a 64-bit division, and goes element by
+// element where a row ends in its 16 bytes.
 #include "device_common.h"
 #include "muon_internal.h"
 
