@@ -1239,11 +1239,13 @@ void name_phases(muon_handle_t h) {
 }
 
 // Body shared by muon_init and muon_init_static: `plan` is built and checked
-// against the workspace already.  With `with_streams` false the handle
-// creates no streams or events: every launch of muon_step then runs on the
-// caller's stream.
+// against the workspace already.  static_device: -1, or the GPU whose static
+// array the workspace is; such a handle creates no streams or events (every
+// launch of muon_step then runs on the caller's stream) and supersedes the
+// earlier ones once all that can fail on the host is done.
 muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* tensors, int32_t n_tensors,
-                          const muon_hparams_t* hp, void* workspace, void* stream, bool with_streams) {
+                          const muon_hparams_t* hp, void* workspace, void* stream, int static_device) {
+  const bool with_streams = static_device < 0;
   std::string who;
   if (overlaps_tensors(workspace, plan.total, tensors, size_t(n_tensors), &who))
     return fail(MUON_ERR_ALIASING, who + " overlaps the workspace");
@@ -1265,6 +1267,11 @@ muon_status_t init_handle(muon_handle_t* out, Plan&& plan, const muon_tensor_t* 
   if (!with_streams) max_lane = 0;
   h->lane_streams.reserve(size_t(max_lane));
   h->ev_joins.reserve(size_t(max_lane));
+  if (static_device >= 0) {
+    std::lock_guard<std::mutex> lk(g_static_mu);
+    h->static_device = static_device;
+    h->static_generation = ++g_static_gen[static_device];
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipMemsetAsync(h->ws, 0, h->plan.total, s);
   if (e == hipSuccess) e = hipMemcpyAsync(h->ws, h->meta.data(), h->meta.size(), hipMemcpyHostToDevice, s);
@@ -1323,7 +1330,7 @@ muon_status_t muon_init(muon_handle_t* out, const muon_tensor_t* tensors, int32_
     if (workspace_bytes < plan.total)
       return fail(MUON_ERR_WORKSPACE_TOO_SMALL,
                   "workspace has " + std::to_string(workspace_bytes) + " bytes, needs " + std::to_string(plan.total));
-    return init_handle(out, std::move(plan), tensors, n_tensors, hp, workspace, stream, true);
+    return init_handle(out, std::move(plan), tensors, n_tensors, hp, workspace, stream, -1);
   });
 }
 
@@ -1345,16 +1352,7 @@ muon_status_t muon_init_static(muon_handle_t* out, const muon_tensor_t* tensors,
     int dev = -1;
     void* ptr = nullptr;
     if ((st = static_scratch(&dev, &ptr)) != MUON_OK) return st;
-    uint64_t gen;
-    {
-      std::lock_guard<std::mutex> lk(g_static_mu);
-      gen = ++g_static_gen[dev];
-    }
-    st = init_handle(out, std::move(plan), tensors, n_tensors, hp, ptr, stream, false);
-    if (st != MUON_OK) return st;
-    (*out)->static_device = dev;
-    (*out)->static_generation = gen;
-    return MUON_OK;
+    return init_handle(out, std::move(plan), tensors, n_tensors, hp, ptr, stream, dev);
   });
 }
 

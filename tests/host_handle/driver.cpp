@@ -59,6 +59,11 @@ hipError_t hipEventRecord(hipEvent_t, hipStream_t) { return hipSuccess; }
 hipError_t hipEventSynchronize(hipEvent_t) { return hipSuccess; }
 hipError_t hipEventElapsedTime(float* ms, hipEvent_t, hipEvent_t) { return *ms = 1.f, hipSuccess; }
 hipError_t hipStreamWaitEvent(hipStream_t, hipEvent_t, unsigned int) { return hipSuccess; }
+hipError_t hipGetDevice(int* d) { return *d = 0, hipSuccess; }
+hipError_t hipGetSymbolAddress(void** p, const void*) {
+  *p = reinterpret_cast<void*>(uintptr_t(1) << 40);
+  return hipSuccess;
+}
 const char* hipGetErrorString(hipError_t) { return "stand-in"; }
 int roctxRangePushA(const char*) { return 0; }
 int roctxRangePop() { return 0; }
@@ -301,11 +306,51 @@ static void check_names() {
   (void)muon_destroy(h);
 }
 
+// A static init that fails before it touches the array leaves the earlier handle as it was.
+static void check_static() {
+  Request r;
+  r.tensors.erase(r.tensors.begin() + 1, r.tensors.begin() + 8);     // what fits the array
+  const auto init = [&](muon_handle_t* h) {
+    return muon_init_static(h, r.tensors.data(), int32_t(r.tensors.size()), &r.slot, 1, &r.hp, nullptr);
+  };
+  muon_handle_t first = nullptr, second = nullptr;
+  long n = g_news;
+  CHECK(init(&first) == MUON_OK, "init: %s", muon_last_error());
+  n = g_news - n;
+  CHECK(muon_step(first, -1.f, nullptr) == MUON_OK, "step: %s", muon_last_error());
+  const void* const grad = r.tensors[0].grad;
+  r.tensors[0].grad = reinterpret_cast<void*>((uintptr_t(1) << 40) + 4096);     // inside the array
+  CHECK(init(&second) == MUON_ERR_ALIASING && !second, "aliasing");
+  r.tensors[0].grad = grad;
+  CHECK(muon_step(first, -1.f, nullptr) == MUON_OK, "after an aliasing init: %s", muon_last_error());
+  for (long k = 1; k <= n; ++k) {
+    g_fail_at = k;
+    const muon_status_t st = init(&second);
+    g_fail_at = 0;
+    if (st == MUON_OK) {                       // a sort that does without its copy: this one took over
+      (void)muon_destroy(first);
+      first = second;
+      second = nullptr;
+    }
+    if (muon_step(first, -1.f, nullptr) != MUON_OK) {
+      CHECK(false, "allocation %ld: %s", k, muon_last_error());
+      (void)muon_destroy(first);
+      if (init(&first) != MUON_OK) return;
+    }
+  }
+  CHECK(init(&second) == MUON_OK, "init: %s", muon_last_error());
+  CHECK(muon_step(first, -1.f, nullptr) == MUON_ERR_BAD_ARG, "a superseded handle steps");
+  CHECK(muon_step(second, -1.f, nullptr) == MUON_OK, "step: %s", muon_last_error());
+  (void)muon_destroy(first);
+  (void)muon_destroy(second);
+}
+
 int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "init") check_init();
   else if (what == "exceptions") check_exceptions();
   else if (what == "names") check_names();
+  else if (what == "static") check_static();
   else return 2;
   if (!g_bad) std::printf("ok\n");
   return g_bad ? 1 : 0;

@@ -37,7 +37,7 @@ def driver(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("what", ["names", "init", "exceptions"])
+@pytest.mark.parametrize("what", ["names", "init", "exceptions", "static"])
 def test_handle(driver, what):
     r = subprocess.run([driver, what], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.splitlines()[-1:] == ["ok"], r.stdout[-4000:]
