@@ -320,6 +320,59 @@ muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed);
 muon_status_t muon_pack_moments(muon_handle_t h, const void* values, int32_t dtype, void* stream);
 muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, void* stream);
 
+/* Microscaled 4-bit floats (MXFP4): a number is one of 0, 0.5, 1, 1.5, 2, 3, 4
+ * and 6 with a sign (e2m1) times its block's scale 2^(e-127), one byte e for 32
+ * consecutive elements.  A matrix may be held in blocks along its rows, along
+ * its columns, or in both forms; the form along the columns is that of the
+ * transpose, so in either form a block's codes and the blocks of one line
+ * follow each other in memory:
+ *   codes    line i at codes + i * ld_codes, 16 bytes a block, two elements a
+ *            byte, the first in the lower four bits: sign in bit 3, then the
+ *            magnitude's place in the list above
+ *   scales   line i at scales + i * ld_scales, one byte a block
+ * A line's last block is filled up with zeros.  A codes pointer and its leading
+ * dimension (bytes) are multiples of 16, a scales pointer and its leading
+ * dimension of 4.  Bytes between a line's last block and the next line are
+ * neither read for their value nor written.
+ *   scale     the smallest with which no element of the block is beyond 6
+ *             scales, at least 2^-127 and at most 2^125 (a magnitude above
+ *             1.5 * 2^127 is then held as that); e = 0 where all are zero
+ *   nearest   ties to the even code
+ *   random    up or down such that the mean is the value itself (MUON_ROUND_
+ *             RANDOM): a / step + r / 2^22 rounded down, a the magnitude in
+ *             scales, step the distance of the numbers in a's binade (0.5 below
+ *             2), r the upper 22 bits of a word that is a function of (seed,
+ *             place in the list, row, column), the same for both forms
+ * A block with an element that is not finite has e = 255 and zero codes, and
+ * reads back as NaN throughout.  Reading back is exact, in float32 and bf16. */
+typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_RANDOM = 1 } muon_rounding_t;
+
+typedef struct {
+  void* values;              /* rows x cols, dtype; element (i, j) at i*ld + j  */
+  int64_t rows, cols, ld;    /* rows and cols in [1, 2^30]                      */
+  int32_t dtype;             /* muon_dtype_t of values                          */
+  int32_t reserved;          /* 0                                               */
+  uint8_t* row_codes;        /* blocks along the rows: rows lines; both NULL:   */
+  uint8_t* row_scales;       /*   no such form                                  */
+  int64_t ld_row_codes, ld_row_scales;   /* bytes                               */
+  uint8_t* col_codes;        /* blocks along the columns: cols lines; both      */
+  uint8_t* col_scales;       /*   NULL: no such form                            */
+  int64_t ld_col_codes, ld_col_scales;
+} muon_mx4_t;
+
+/* Rounds each matrix of the list to the forms it names (at least one), both from
+ * one read; one launch for up to 44 matrices of one dtype and one choice of
+ * forms.  Needs no handle; works on the calling thread's current device,
+ * asynchronous on `stream`.  The forms' spans must not overlap each other or any
+ * values of the list.  `seed` is of use only for MUON_ROUND_RANDOM. */
+muon_status_t muon_mx4_quantize(const muon_mx4_t* list, int32_t n, int32_t rounding, uint64_t seed, void* stream);
+
+/* Writes the values that each matrix's form along its rows (axis 1) or columns
+ * (axis 0) stands for; the other form may be NULL.  Otherwise as
+ * muon_mx4_quantize; the values' spans must not overlap each other or the forms
+ * read. */
+muon_status_t muon_mx4_dequantize(const muon_mx4_t* list, int32_t n, int32_t axis, void* stream);
+
 /* Clipping by the global norm: with max_norm > 0 every following muon_step
  * computes norm = sqrt(sum of the squares of every registered gradient, Muon
  * and AdamW) in float64 and multiplies each gradient by

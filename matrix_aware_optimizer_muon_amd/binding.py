@@ -28,6 +28,7 @@ MUON_F32, MUON_BF16 = 0, 1
 SCALE_NONE, SCALE_ORIGINAL, SCALE_MATCH_RMS_ADAMW, SCALE_SPECTRAL = 0, 1, 2, 3
 MOM_EMA, MOM_SGD = 0, 1
 KIND_MUON, KIND_ADAMW = 0, 1
+ROUNDINGS = {"nearest": 0, "random": 1}
 
 
 class MuonTensor(ctypes.Structure):
@@ -62,6 +63,17 @@ class MuonHparams(ctypes.Structure):
         ("scale_mode", ctypes.c_int32), ("momentum_form", ctypes.c_int32),
         ("adam_lr", ctypes.c_float), ("adam_beta1", ctypes.c_float), ("adam_beta2", ctypes.c_float),
         ("adam_eps", ctypes.c_float), ("adam_weight_decay", ctypes.c_float),
+    ]
+
+
+class MuonMx4(ctypes.Structure):
+    _fields_ = [
+        ("values", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("row_codes", ctypes.c_void_p), ("row_scales", ctypes.c_void_p),
+        ("ld_row_codes", ctypes.c_int64), ("ld_row_scales", ctypes.c_int64),
+        ("col_codes", ctypes.c_void_p), ("col_scales", ctypes.c_void_p),
+        ("ld_col_codes", ctypes.c_int64), ("ld_col_scales", ctypes.c_int64),
     ]
 
 
@@ -115,6 +127,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_set_max_grad_norm": (i32, [vp, f32, vp]),
         "muon_pack_moments": (i32, [vp, vp, i32, vp]),
         "muon_unpack_moments": (i32, [vp, vp, i32, vp]),
+        "muon_mx4_quantize": (i32, [ctypes.POINTER(MuonMx4), i32, i32, ctypes.c_uint64, vp]),
+        "muon_mx4_dequantize": (i32, [ctypes.POINTER(MuonMx4), i32, i32, vp]),
         "muon_destroy": (i32, [vp]),
         "muon_plan_describe": (i32, [PT, i32, PP, i32, PH, ctypes.c_char_p, sz, ctypes.POINTER(sz)]),
         "muon_status_str": (ctypes.c_char_p, [i32]),
@@ -134,7 +148,7 @@ def header_functions() -> List[str]:
     with open(HEADER_PATH) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(muon_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(muon_[a-z0-9_]+)\s*\(", text)))
 
 
 def _check(status, lib=None):
@@ -336,6 +350,247 @@ def adam_tensor_desc(param, grad, exp_avg, exp_avg_sq, *, lr_mult=1.0) -> MuonTe
     d.kind = KIND_ADAMW
     d.update_out = None
     return d
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floats
+# ---------------------------------------------------------------------------
+
+def _raw_stream(device, stream):
+    """The hipStream_t of `stream`, or of torch's current one on `device`, which has to be a GPU."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None:
+        return ctypes.c_void_p(raw(device.index))
+    return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _launch_on(device, function, *args):
+    """Call a library function that needs no handle with `device` the current one."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device.index:
+        _check(function(*args))
+    else:
+        with cuda.device(device):
+            _check(function(*args))
+
+
+class Mx4:
+    """A rows x cols matrix held in microscaled 4-bit floats (include/muon.h):
+    axis 1 in blocks of 32 along its rows (`rows` lines), axis 0 along its
+    columns (`cols` lines, those of the transpose).  `codes` is uint8 [lines,
+    >= 16 * blocks] and `scales` uint8 [lines, >= blocks], on one device, each
+    with unit stride in a line; lines begin at multiples of 16 and 4 bytes."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "axis")
+
+    def __init__(self, codes, scales, rows, cols, axis=1):
+        if axis not in (0, 1):
+            raise ValueError("axis is 1 (blocks along the rows) or 0 (along the columns)")
+        lines, length = (rows, cols) if axis == 1 else (cols, rows)
+        blocks = -(-length // 32)
+        for t, width, name in ((codes, 16 * blocks, "codes"), (scales, blocks, "scales")):
+            if t.dtype != _torch().uint8 or t.dim() != 2 or t.shape[0] != lines or t.shape[1] < width:
+                raise ValueError(f"{name} must be uint8 of shape ({lines}, {width} or more)")
+            if t.shape[1] > 1 and t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < width):
+                raise ValueError(f"{name} must have unit stride in a line and lines apart")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.rows, self.cols, self.axis = codes, scales, rows, cols, axis
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _leading(self):
+        """Bytes between lines of codes and of scales (a single line's own width: its stride says nothing)."""
+        return [t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
+                for t, unit in ((self.codes, 16), (self.scales, 4))]
+
+    def _describe(self, d):
+        ld_codes, ld_scales = self._leading()
+        if self.axis == 1:
+            d.row_codes, d.row_scales = self.codes.data_ptr(), self.scales.data_ptr()
+            d.ld_row_codes, d.ld_row_scales = ld_codes, ld_scales
+        else:
+            d.col_codes, d.col_scales = self.codes.data_ptr(), self.scales.data_ptr()
+            d.ld_col_codes, d.ld_col_scales = ld_codes, ld_scales
+
+    def record_stream(self, stream):
+        self.codes.record_stream(stream)
+        self.scales.record_stream(stream)
+
+
+def mx4_empty(rows, cols, axis=1, device=None) -> Mx4:
+    """Memory for a rows x cols matrix in 4 bits (contents undefined)."""
+    torch = _torch()
+    lines, length = (rows, cols) if axis == 1 else (cols, rows)
+    blocks = -(-length // 32)
+    device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+    scales = torch.empty((lines, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
+    return Mx4(torch.empty((lines, 16 * blocks), dtype=torch.uint8, device=device), scales, rows, cols, axis)
+
+
+def _mx4_values(x):
+    """A tensor as the matrix that its 4-bit forms are those of (a vector as 1 x n, more dimensions as shape[0] x
+    rest), and the ABI's dtype of its elements."""
+    torch = _torch()
+    dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    x = _adam_matrix(x)
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError("tensors must be row-major (unit column stride)")
+    return x, dt
+
+
+def mx4_desc(values, *forms) -> MuonMx4:
+    """The ABI's description of a matrix with its forms (at most one each way)."""
+    x, dt = _mx4_values(values)
+    d = MuonMx4()
+    d.values, d.dtype = x.data_ptr(), dt
+    d.rows, d.cols = x.shape
+    d.ld = x.stride(0) if x.shape[0] > 1 else d.cols
+    for f in forms:
+        if (f.rows, f.cols) != tuple(x.shape):
+            raise ValueError(f"a form of a {f.rows} x {f.cols} matrix for one of {d.rows} x {d.cols}")
+        if f.device != x.device:
+            raise ValueError("values and forms must be on one device")
+        f._describe(d)
+    return d
+
+
+def _rounding(rounding):
+    if rounding not in ROUNDINGS:
+        raise ValueError(f"rounding is one of {sorted(ROUNDINGS)}")
+    return ROUNDINGS[rounding]
+
+
+def _seed64(seed):
+    return ctypes.c_uint64(int(seed) & (2 ** 64 - 1))
+
+
+def mx4_quantize(x, axis=1, out: Optional[Mx4] = None, rounding: str = "nearest", seed: int = 0, stream=None) -> Mx4:
+    """`x` (float32 or bfloat16, any shape, viewed as _adam_matrix does) in
+    microscaled 4-bit floats, in blocks along its rows (axis 1) or columns
+    (axis 0), rounded to nearest or at random (a function of `seed`); into
+    `out` if given (whose axis then counts)."""
+    torch = _torch()
+    mode = _rounding(rounding)
+    m, _ = _mx4_values(x)
+    given = out is not None
+    if not given:
+        with torch.cuda.stream(stream):       # of that stream's memory (None: the current one's)
+            out = mx4_empty(m.shape[0], m.shape[1], axis, x.device)
+    d = mx4_desc(x, out)
+    _launch_on(x.device, load_library().muon_mx4_quantize, ctypes.byref(d), 1, mode, _seed64(seed),
+               _raw_stream(x.device, stream))
+    if stream is not None:
+        x.record_stream(stream)
+        out.record_stream(stream if given else torch.cuda.current_stream(x.device))
+    return out
+
+
+def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
+    """The values that `q` stands for, exactly, as a rows x cols tensor of
+    `dtype` (float32, the default, or bfloat16); into `out` if given."""
+    torch = _torch()
+    given = out is not None
+    if not given:
+        with torch.cuda.stream(stream):
+            out = torch.empty((q.rows, q.cols), dtype=dtype or torch.float32, device=q.device)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError("out is not of the dtype asked for")
+    d = mx4_desc(out, q)
+    _launch_on(q.device, load_library().muon_mx4_dequantize, ctypes.byref(d), 1, q.axis, _raw_stream(q.device, stream))
+    if stream is not None:
+        q.record_stream(stream)
+        out.record_stream(stream if given else torch.cuda.current_stream(q.device))
+    return out
+
+
+class Mx4Copies:
+    """The 4-bit copies of a list of tensors (a model's weights), each way that
+    `axis` names: 1 along the rows, 0 along the columns, or (1, 0).  The
+    tensors must stay where they are while the object is used.  `copies[k]` is
+    the k-th tensor's tuple of Mx4, in the order of `axis`."""
+
+    def __init__(self, tensors, axis=(1, 0)):
+        torch = _torch()
+        self.axes = tuple(axis) if isinstance(axis, (tuple, list)) else (axis,)
+        if not self.axes or len(set(self.axes)) != len(self.axes) or not set(self.axes) <= {0, 1}:
+            raise ValueError("axis is 1, 0 or both")
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.device = self.tensors[0].device
+        if any(t.device != self.device for t in self.tensors):
+            raise ValueError("the tensors must be on one device")
+        shapes = [tuple(_mx4_values(t)[0].shape) for t in self.tensors]
+        # one buffer for all copies, each part of it from a multiple of 256 bytes on
+        sizes = []
+        for rows, cols in shapes:
+            for a in self.axes:
+                lines, blocks = (rows, -(-cols // 32)) if a == 1 else (cols, -(-rows // 32))
+                sizes += [(lines, 16 * blocks), (lines, -(-blocks // 4) * 4)]
+        starts, total = [], 0
+        for lines, width in sizes:
+            starts.append(total)
+            total += -(-lines * width // 256) * 256
+        buffer = torch.empty(total, dtype=torch.uint8, device=self.device)
+        parts = iter([buffer[at:at + lines * width].view(lines, width) for at, (lines, width) in zip(starts, sizes)])
+        self.copies = [tuple(Mx4(next(parts), next(parts), rows, cols, a) for a in self.axes) for rows, cols in shapes]
+        self.elements = sum(r * c for r, c in shapes)
+        self._shapes = shapes
+        self._descs, self._n = _array([mx4_desc(t, *c) for t, c in zip(self.tensors, self.copies)], MuonMx4)
+        self._values, _ = _array(self._descs[:self._n], MuonMx4)        # with the values elsewhere: dequantize
+        for d in self._values[:self._n]:
+            d.ld = d.cols
+
+    def quantize(self, rounding: str = "nearest", seed: int = 0, stream=None):
+        """Renew every copy from its tensor."""
+        _launch_on(self.device, load_library().muon_mx4_quantize, self._descs, self._n, _rounding(rounding),
+                   _seed64(seed), _raw_stream(self.device, stream))
+
+    def dequantize(self, axis: Optional[int] = None, dtype=None, out=None, stream=None):
+        """The values of every copy along `axis` (default: the first one),
+        exactly, one tensor's after another's in a vector of `elements`
+        numbers of `dtype` (float32, the default, or bfloat16); into `out` if
+        given.  `split` cuts it into the tensors' own."""
+        torch = _torch()
+        axis = self.axes[0] if axis is None else axis
+        if axis not in self.axes:
+            raise ValueError("no copies along that axis")
+        given = out is not None
+        if not given:
+            with torch.cuda.stream(stream):
+                out = torch.empty(self.elements, dtype=dtype or torch.float32, device=self.device)
+        elif dtype is not None and dtype != out.dtype:
+            raise ValueError("out is not of the dtype asked for")
+        elif out.shape != (self.elements,) or not out.is_contiguous() or out.device != self.device:
+            raise ValueError(f"out must be a contiguous vector of {self.elements} elements on {self.device}")
+        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(out.dtype)
+        if dt is None:
+            raise ValueError(f"unsupported dtype {out.dtype}")
+        at, es = out.data_ptr(), out.element_size()
+        for d in self._values[:self._n]:
+            d.values, d.dtype = at, dt
+            at += d.rows * d.cols * es
+        _launch_on(self.device, load_library().muon_mx4_dequantize, self._values, self._n, axis,
+                   _raw_stream(self.device, stream))
+        if stream is not None:
+            out.record_stream(stream if given else torch.cuda.current_stream(self.device))
+        return out
+
+    def split(self, values):
+        """Views of `values` (dequantize's layout) by tensor, each rows x cols."""
+        out, at = [], 0
+        for rows, cols in self._shapes:
+            out.append(values[at:at + rows * cols].view(rows, cols))
+            at += rows * cols
+        return out
 
 
 class MuonStep:

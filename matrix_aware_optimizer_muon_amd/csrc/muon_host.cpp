@@ -1609,6 +1609,150 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
   });
 }
 
+namespace {
+
+// One launch over matrices of one dtype and one choice of forms.
+struct Mx4Launch {
+  Mx4List list;
+  bool f32, row, col;
+};
+
+// A span of memory that a call on a list touches.
+struct Mx4Span { uintptr_t lo, hi; bool written; int32_t matrix; const char* what; };
+
+// One form's lines: their addresses, alignment and span.
+muon_status_t check_mx4_form(const std::string& who, const char* what, const uint8_t* codes, const uint8_t* scales,
+                             int64_t ld_codes, int64_t ld_scales, int64_t lines, int64_t length, bool written,
+                             int32_t matrix, std::vector<Mx4Span>& spans) {
+  if (!codes || !scales) return fail(MUON_ERR_NULL_ARG, who + what + ": codes and scales go together");
+  const int64_t blocks = (length + kMx4Block - 1) / kMx4Block;
+  if (ld_codes < blocks * 16 || ld_scales < blocks)
+    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions below a line's blocks");
+  if (ld_codes > int64_t(16) << 31 || ld_scales > int64_t(4) << 31)
+    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions too large");
+  if (reinterpret_cast<uintptr_t>(codes) % 16 || ld_codes % 16 || reinterpret_cast<uintptr_t>(scales) % 4 || ld_scales % 4)
+    return fail(MUON_ERR_ALIGNMENT, who + what + ": codes and their leading dimension are multiples of 16, scales of 4");
+  const uintptr_t c = reinterpret_cast<uintptr_t>(codes), e = reinterpret_cast<uintptr_t>(scales);
+  spans.push_back({c, c + uintptr_t((lines - 1) * ld_codes + blocks * 16), written, matrix, "codes"});
+  spans.push_back({e, e + uintptr_t((lines - 1) * ld_scales + blocks), written, matrix, "scales"});
+  return MUON_OK;
+}
+
+// Checks a list and cuts it into launches.  axis -1: quantising (both forms, where given); else the form read.
+muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vector<Mx4Launch>& out) {
+  if (n < 0) return fail(MUON_ERR_BAD_ARG, "n < 0");
+  if (n > 0 && !list) return fail(MUON_ERR_NULL_ARG, "list is NULL");
+  const bool quantize = axis < 0;
+  std::vector<Mx4Span> spans;
+  spans.reserve(size_t(n) * 5);
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_mx4_t& x = list[i];
+    const std::string who = "matrix " + std::to_string(i) + ": ";
+    if (!x.values) return fail(MUON_ERR_NULL_ARG, who + "values is NULL");
+    if (x.dtype != MUON_F32 && x.dtype != MUON_BF16) return fail(MUON_ERR_BAD_DTYPE, who + "dtype must be MUON_F32 or MUON_BF16");
+    constexpr int64_t most = int64_t(1) << 30;
+    if (x.rows < 1 || x.cols < 1 || x.rows > most || x.cols > most)
+      return fail(MUON_ERR_BAD_SHAPE, who + "rows and cols must be in [1, 2^30]");
+    if (x.ld < x.cols) return fail(MUON_ERR_BAD_SHAPE, who + "the leading dimension must be >= cols");
+    if (x.reserved != 0) return fail(MUON_ERR_BAD_ARG, who + "reserved must be 0");
+    const size_t es = x.dtype == MUON_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail(MUON_ERR_ALIGNMENT, who + "values misaligned");
+    const bool row = axis != 0 && (x.row_codes || x.row_scales || axis == 1);
+    const bool col = axis != 1 && (x.col_codes || x.col_scales || axis == 0);
+    if (!row && !col) return fail(MUON_ERR_NULL_ARG, who + "no form is given");
+    muon_status_t st = MUON_OK;
+    if (row) st = check_mx4_form(who, "form along the rows", x.row_codes, x.row_scales, x.ld_row_codes, x.ld_row_scales,
+                                 x.rows, x.cols, quantize, i, spans);
+    if (st == MUON_OK && col)
+      st = check_mx4_form(who, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales,
+                          x.cols, x.rows, quantize, i, spans);
+    if (st != MUON_OK) return st;
+    const uintptr_t v = reinterpret_cast<uintptr_t>(x.values);
+    spans.push_back({v, v + uintptr_t((x.rows - 1) * x.ld + x.cols) * es, !quantize, i, "values"});
+    const bool f32 = x.dtype == MUON_F32;
+    Mx4Dev d;
+    std::memset(&d, 0, sizeof(d));
+    d.values = x.values;
+    d.ld = x.ld;
+    d.rows = int32_t(x.rows);
+    d.cols = int32_t(x.cols);
+    d.index = uint32_t(i);
+    d.vec = v % 16 == 0 && (x.rows == 1 || (x.ld * int64_t(es)) % 16 == 0);
+    d.tiles_c = int32_t((x.cols + kMx4Tile - 1) / kMx4Tile);
+    if (row) {
+      d.row = {x.row_codes, x.row_scales};
+      d.row_ld16 = uint32_t(x.ld_row_codes / 16);
+      d.row_ld4 = uint32_t(x.ld_row_scales / 4);
+    }
+    if (col) {
+      d.col = {x.col_codes, x.col_scales};
+      d.col_ld16 = uint32_t(x.ld_col_codes / 16);
+      d.col_ld4 = uint32_t(x.ld_col_scales / 4);
+    }
+    const int64_t tiles = (x.rows + kMx4Tile - 1) / kMx4Tile * d.tiles_c;
+    if (tiles > kMx4MaxTiles) return fail(MUON_ERR_UNSUPPORTED, who + "more than 2^24 - 1 tiles of 128 x 128");
+    Mx4Launch* to = nullptr;    // the latest launch of this kind, if it has room
+    for (Mx4Launch& k : out)
+      if (k.f32 == f32 && k.row == row && k.col == col) to = &k;
+    if (!to || to->list.n == kMx4Most || to->list.tiles + tiles > kMx4MaxTiles) {
+      out.emplace_back();
+      to = &out.back();
+      to->f32 = f32;
+      to->row = row;
+      to->col = col;
+      to->list.n = to->list.tiles = 0;
+    }
+    d.tile0 = to->list.tiles;
+    to->list.m[to->list.n++] = d;
+    to->list.tiles += int32_t(tiles);
+  }
+  // what is written overlaps nothing; what is read may be read twice
+  std::sort(spans.begin(), spans.end(), [](const Mx4Span& a, const Mx4Span& b) { return a.lo < b.lo; });
+  const Mx4Span *any = nullptr, *written = nullptr;     // of those before, the ones that end last
+  for (const Mx4Span& x : spans) {
+    const Mx4Span* const hit = x.written ? any : written;
+    if (hit && x.lo < hit->hi)
+      return fail(MUON_ERR_ALIASING, std::string("buffers overlap: matrix ") + std::to_string(hit->matrix) + " " + hit->what +
+                                         " and matrix " + std::to_string(x.matrix) + " " + x.what);
+    if (!any || x.hi > any->hi) any = &x;
+    if (x.written && (!written || x.hi > written->hi)) written = &x;
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+
+muon_status_t muon_mx4_quantize(const muon_mx4_t* list, int32_t n, int32_t rounding, uint64_t seed, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    if (rounding != MUON_ROUND_NEAREST && rounding != MUON_ROUND_RANDOM) return fail(MUON_ERR_BAD_ARG, "unknown rounding");
+    std::vector<Mx4Launch> launches;
+    const muon_status_t st = mx4_launches(list, n, -1, launches);
+    if (st != MUON_OK) return st;
+    Range r("muon.mx4_quantize");
+    for (const Mx4Launch& k : launches) {
+      const hipError_t e = launch_mx4_quantize(k.list, k.f32, rounding == MUON_ROUND_RANDOM,
+                                               {uint32_t(seed), uint32_t(seed >> 32)}, static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("mx4 quantize launch: ") + hipGetErrorString(e));
+    }
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_mx4_dequantize(const muon_mx4_t* list, int32_t n, int32_t axis, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    if (axis != 0 && axis != 1) return fail(MUON_ERR_BAD_ARG, "axis must be 0 (columns) or 1 (rows)");
+    std::vector<Mx4Launch> launches;
+    const muon_status_t st = mx4_launches(list, n, axis, launches);
+    if (st != MUON_OK) return st;
+    Range r("muon.mx4_dequantize");
+    for (const Mx4Launch& k : launches) {
+      const hipError_t e = launch_mx4_dequantize(k.list, k.f32, axis, static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("mx4 dequantize launch: ") + hipGetErrorString(e));
+    }
+    return MUON_OK;
+  });
+}
+
 muon_status_t muon_get_flags(muon_handle_t h, void* stream, int32_t reset, uint32_t* flags) {
   return guarded([&]() -> muon_status_t {
     if (!h || !flags) return fail(MUON_ERR_NULL_ARG, "handle or flags is NULL");

@@ -229,6 +229,26 @@ struct PackedParams {
   RoundingSeed seed;
 };
 
+// Microscaled 4-bit floats (mx4.hip has the format).  A list of matrices
+// travels in the kernel's arguments, so a call needs no device memory and a
+// captured one keeps its list.
+constexpr int kMx4Block = 32;
+constexpr int kMx4Tile = 128;          // a thread block's tile: rows and columns
+constexpr int kMx4Most = 44;           // matrices of a launch: 4 KB of arguments
+constexpr int64_t kMx4MaxTiles = (int64_t(1) << 24) - 1;   // of a launch: below 2^32 threads
+struct Mx4Form { uint8_t* codes; uint8_t* scales; };
+struct Mx4Dev {
+  void* values; int64_t ld;
+  Mx4Form row, col;
+  uint32_t row_ld16, row_ld4, col_ld16, col_ld4;   // of codes in 16 bytes, of scales in 4
+  int32_t rows, cols;
+  int32_t tile0, tiles_c;              // tiles of the matrices before this one; tiles across
+  uint32_t index;                      // its place in the caller's list (random words)
+  int32_t vec;                         // rows of values 16-byte aligned
+};
+struct Mx4List { Mx4Dev m[kMx4Most]; int32_t n, tiles; };
+static_assert(sizeof(Mx4List) + 64 <= 4096, "kernel arguments");
+
 // Global gradient norm: every registered gradient as a run of n elements cut
 // in chunks of kNormChunk, the chunks of all tensors numbered through; block b
 // of n sums chunks b, b + n and so on.
@@ -301,5 +321,8 @@ MUON_WEAK hipError_t launch_unpack_moments(const PackedDev* tensors, const Packe
                                            void* values, int64_t n_values, bool f32, uint32_t* flags,
                                            hipStream_t s);
 MUON_WEAK hipError_t launch_grad_norm(const NormParams& p, hipStream_t s);
+// the matrices of a list share dtype and forms; axis: 1 the form along the rows is read, 0 along the columns
+MUON_WEAK hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, RoundingSeed seed, hipStream_t s);
+MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, hipStream_t s);
 
 }  // namespace muon
