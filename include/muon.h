@@ -235,6 +235,28 @@ muon_status_t muon_precond_accumulate(muon_handle_t h, int32_t slot, int32_t blo
 muon_status_t muon_precond_refresh_accumulated(muon_handle_t h, int32_t slot, int32_t block, float damping,
                                                int32_t reset, void* stream);
 
+/* Both calls for activations held in microscaled 4-bit floats (below) with
+ * blocks along the samples, the form along the columns of the n_rows x d
+ * activations: line i of codes and scales is feature i, ld_codes and ld_scales
+ * bytes from the next; n_rows in [1, 2^30].  Otherwise as
+ * muon_precond_refresh and muon_precond_accumulate, but for beta in float64:
+ * Sigma and N are decayed by the same factor, in float64, Sigma then rounded.
+ * The products are exact in float32 and summed in it.  What lies behind the n_rows-th sample of a line is
+ * not counted. */
+muon_status_t muon_precond_refresh_mx4(muon_handle_t h, int32_t slot, int32_t block, const uint8_t* codes,
+                                       const uint8_t* scales, int64_t n_rows, int64_t ld_codes, int64_t ld_scales,
+                                       float damping, void* stream);
+muon_status_t muon_precond_accumulate_mx4(muon_handle_t h, int32_t slot, int32_t block, const uint8_t* codes,
+                                          const uint8_t* scales, int64_t n_rows, int64_t ld_codes, int64_t ld_scales,
+                                          double beta, void* stream);
+
+/* Where the running sums of a block lie, in the handle's workspace: Sigma, d x d
+ * float32 with leading dimension *ld, symmetric, and N, one float64 (each
+ * pointer may be NULL).  Host only.  To be read and written in the order of the
+ * stream that the handle is used on: for a checkpoint, or to add up the sums of
+ * data-parallel ranks before a refresh. */
+muon_status_t muon_precond_sums(muon_handle_t h, int32_t slot, int32_t block, float** sums, int64_t* ld, double** count);
+
 /* One optimizer step over every registered tensor: Muon on the kind-MUON
  * matrices (lr < 0 uses hp.lr), AdamW on the kind-ADAMW tensors (hp.adam_lr).
  * Asynchronous on `stream`; no allocation, no synchronisation.  Part of the
@@ -252,7 +274,8 @@ muon_status_t muon_step(muon_handle_t h, float lr, void* stream);
  * (at most max_phases are written).  Every launch runs on `stream`, one
  * after the other (no lanes), so each phase's time is that launch's alone.
  * For profiling only.  With a maximum norm set (muon_set_max_grad_norm) phase 0
- * is the norm's, "grad_norm", and the others come one later.  A name stays
+ * is the norm's, "grad_norm", and the others come one later; with 4-bit copies
+ * set (muon_set_mx4_weights) "mx4_weights" is the last one.  A name stays
  * where it is until muon_destroy(). */
 muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream,
                               float* phase_ms, int32_t max_phases, int32_t* n_phases);
@@ -372,6 +395,16 @@ muon_status_t muon_mx4_quantize(const muon_mx4_t* list, int32_t n, int32_t round
  * muon_mx4_quantize; the values' spans must not overlap each other or the forms
  * read. */
 muon_status_t muon_mx4_dequantize(const muon_mx4_t* list, int32_t n, int32_t axis, void* stream);
+
+/* 4-bit copies of registered weights, renewed by every following muon_step as
+ * its last launches, from the weights that the step has written (rounded to
+ * nearest).  Each entry names a registered tensor by its values, rows, cols, ld
+ * and dtype (those of the param) and the forms to fill, which lie apart from the
+ * registered tensors and the workspace and stay allocated while they are set; a
+ * captured step keeps the ones that it was captured with.  n = 0 switches it off.
+ * Host only: the copies hold the weights from the next step on
+ * (muon_mx4_quantize of the same list fills them before). */
+muon_status_t muon_set_mx4_weights(muon_handle_t h, const muon_mx4_t* copies, int32_t n);
 
 /* Clipping by the global norm: with max_norm > 0 every following muon_step
  * computes norm = sqrt(sum of the squares of every registered gradient, Muon

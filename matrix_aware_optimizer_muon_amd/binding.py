@@ -127,6 +127,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_set_max_grad_norm": (i32, [vp, f32, vp]),
         "muon_pack_moments": (i32, [vp, vp, i32, vp]),
         "muon_unpack_moments": (i32, [vp, vp, i32, vp]),
+        "muon_precond_refresh_mx4": (i32, [vp, i32, i32, vp, vp, i64, i64, i64, f32, vp]),
+        "muon_precond_accumulate_mx4": (i32, [vp, i32, i32, vp, vp, i64, i64, i64, ctypes.c_double, vp]),
+        "muon_precond_sums": (i32, [vp, i32, i32, ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(vp)]),
+        "muon_set_mx4_weights": (i32, [vp, ctypes.POINTER(MuonMx4), i32]),
         "muon_mx4_quantize": (i32, [ctypes.POINTER(MuonMx4), i32, i32, ctypes.c_uint64, vp]),
         "muon_mx4_dequantize": (i32, [ctypes.POINTER(MuonMx4), i32, i32, vp]),
         "muon_destroy": (i32, [vp]),
@@ -700,31 +704,60 @@ class MuonStep:
                      ctypes.byref(n))
         return [(self._lib.muon_phase_name(self._h, i).decode(), ms[i]) for i in range(min(n.value, cap))]
 
-    def precond_refresh(self, slot: int, block: int, acts, damping: float = 1e-4, stream=None):
+    def _acts_call(self, name, slot, block, acts, scalar, stream):
+        """One call of muon_precond_<name> on activations: a tensor, or an Mx4 with blocks along the samples."""
         torch = _torch()
-        if acts.dim() != 2 or acts.stride(1) != 1:
-            raise ValueError("activations must be 2-D row-major")
-        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(acts.dtype)
-        if dt is None:
-            raise ValueError(f"unsupported activation dtype {acts.dtype}")
         s = self._torch_stream(stream)
-        self._launch(self._lib.muon_precond_refresh, self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
-                     acts.shape[0], acts.stride(0), dt, ctypes.c_float(damping), ctypes.c_void_p(s.cuda_stream))
+        if isinstance(acts, Mx4):
+            if acts.axis != 0:
+                raise ValueError("activations in 4 bits are held in blocks along the samples (axis 0)")
+            if 0 <= slot < self._npc and acts.cols != self._pcs[slot].d:
+                raise ValueError(f"activations of {acts.cols} features for a slot of {self._pcs[slot].d}")
+            if acts.device != self.device:
+                raise ValueError(f"activations on {acts.device} for a handle on {self.device}")
+            ld_codes, ld_scales = acts._leading()
+            self._launch(getattr(self._lib, f"muon_precond_{name}_mx4"), self._h, slot, block, acts.codes.data_ptr(),
+                         acts.scales.data_ptr(), acts.rows, ld_codes, ld_scales, scalar,
+                         ctypes.c_void_p(s.cuda_stream))
+        else:
+            if acts.dim() != 2 or acts.stride(1) != 1:
+                raise ValueError("activations must be 2-D row-major")
+            dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(acts.dtype)
+            if dt is None:
+                raise ValueError(f"unsupported activation dtype {acts.dtype}")
+            self._launch(getattr(self._lib, f"muon_precond_{name}"), self._h, slot, block,
+                         ctypes.c_void_p(acts.data_ptr()), acts.shape[0], acts.stride(0), dt, ctypes.c_float(scalar),
+                         ctypes.c_void_p(s.cuda_stream))
         self._guard(acts, s)
 
+    def precond_refresh(self, slot: int, block: int, acts, damping: float = 1e-4, stream=None):
+        """Rebuild S^-1 of (slot, block) from layer-input activations, n x d: a
+        float32 or bfloat16 tensor, or an Mx4 with axis 0."""
+        self._acts_call("refresh", slot, block, acts, damping, stream)
+
     def precond_accumulate(self, slot: int, block: int, acts, beta: float = 1.0, stream=None):
-        """Add one micro-batch of layer-input activations to the running
-        second moment of (slot, block): Sigma <- beta Sigma + X^T X."""
+        """Add one micro-batch of layer-input activations (as precond_refresh
+        takes them) to the running second moment of (slot, block):
+        Sigma <- beta Sigma + X^T X."""
+        self._acts_call("accumulate", slot, block, acts, beta, stream)
+
+    def precond_sums(self, slot: int, block: int):
+        """The running second moment of (slot, block) itself, (Sigma, N): views
+        of the workspace, d x d float32 and one float64, to read, write or
+        all-reduce in the order of the handle's stream.  Not for a static
+        handle, whose scratch is no tensor."""
+        if self.workspace is None:
+            raise ValueError("a static handle's sums lie in no tensor")
         torch = _torch()
-        if acts.dim() != 2 or acts.stride(1) != 1:
-            raise ValueError("activations must be 2-D row-major")
-        dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(acts.dtype)
-        if dt is None:
-            raise ValueError(f"unsupported activation dtype {acts.dtype}")
-        s = self._torch_stream(stream)
-        self._launch(self._lib.muon_precond_accumulate, self._h, slot, block, ctypes.c_void_p(acts.data_ptr()),
-                     acts.shape[0], acts.stride(0), dt, ctypes.c_float(beta), ctypes.c_void_p(s.cuda_stream))
-        self._guard(acts, s)
+        sums, count, ld = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_int64()
+        self._check(self._lib.muon_precond_sums(self._h, slot, block, ctypes.byref(sums), ctypes.byref(ld),
+                                                ctypes.byref(count)))
+        d, base = self._pcs[slot].d, self.workspace.data_ptr()
+
+        def view(at, n, dtype):
+            return self.workspace[at - base:at - base + n * dtype.itemsize].view(dtype)
+        rows = view(sums.value, ld.value * ld.value, torch.float32).view(ld.value, ld.value)
+        return rows[:d, :d], view(count.value, 1, torch.float64)
 
     def precond_refresh_accumulated(self, slot: int, block: int, damping: float = 1e-4, reset: bool = True,
                                     stream=None):
@@ -763,6 +796,17 @@ class MuonStep:
         self._check(self._lib.muon_set_max_grad_norm(self._h, ctypes.c_float(max_norm),
                                                 ctypes.c_void_p(out.data_ptr() if out is not None else None)))
         self.grad_norm = out
+
+    def set_mx4_weights(self, copies: Optional[Mx4Copies]):
+        """Renew the 4-bit copies of registered weights at the end of every
+        following step (None: no more).  The tensors of `copies` are those
+        registered as params; copies.quantize() fills them before the first
+        step.  The object lives as long as the handle: a captured step goes on
+        writing to it after it is replaced."""
+        descs, n = (None, 0) if copies is None else (copies._descs, copies._n)
+        self._check(self._lib.muon_set_mx4_weights(self._h, descs, n))
+        if copies is not None and not any(k is copies for k in self._keep):
+            self._keep.append(copies)
 
     def packed_elements(self) -> int:
         """Elements of all tensors with packed moments."""

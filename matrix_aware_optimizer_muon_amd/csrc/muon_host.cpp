@@ -685,9 +685,7 @@ muon_status_t build_plan(const muon_tensor_t* ts, int32_t n, const muon_precond_
   // of the second moment, then the float64 sum of S^-1
   size_t mpart = 0;
   for (const SlotPlan& sp : plan.slots) {
-    const int splits = moment_splits(sp.dp, false, INT64_MAX);   // bf16 tiles split the most
-    const size_t sq = size_t(sp.dp) * sp.dp;
-    mpart = std::max({mpart, sq * sizeof(double), splits > 1 ? size_t(splits) * sq * sizeof(float) : size_t(0)});
+    mpart = std::max(mpart, moment_part_floats(sp.dp) * sizeof(float));
   }
   if (mpart) { plan.off_mpart = off; off = align_up(off + mpart); }
   for (int ti : plan.prec_tensors) {
@@ -844,6 +842,119 @@ std::vector<uint8_t> build_meta(const Plan& plan, const muon_tensor_t* ts, uint8
 
 }  // namespace
 
+namespace {
+
+// One launch over matrices of one dtype and one choice of forms.
+struct Mx4Launch {
+  Mx4List list;
+  bool f32, row, col;
+};
+
+// A span of memory that a call on a list touches.
+struct Mx4Span { uintptr_t lo, hi; bool written; int32_t matrix; const char* what; };
+
+// One form's lines: their addresses, alignment and span.
+muon_status_t check_mx4_form(const std::string& who, const char* what, const uint8_t* codes, const uint8_t* scales,
+                             int64_t ld_codes, int64_t ld_scales, int64_t lines, int64_t length, bool written,
+                             int32_t matrix, std::vector<Mx4Span>& spans) {
+  if (!codes || !scales) return fail(MUON_ERR_NULL_ARG, who + what + ": codes and scales go together");
+  const int64_t blocks = (length + kMx4Block - 1) / kMx4Block;
+  if (ld_codes < blocks * 16 || ld_scales < blocks)
+    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions below a line's blocks");
+  if (ld_codes > int64_t(16) << 31 || ld_scales > int64_t(4) << 31)
+    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions too large");
+  if (reinterpret_cast<uintptr_t>(codes) % 16 || ld_codes % 16 || reinterpret_cast<uintptr_t>(scales) % 4 || ld_scales % 4)
+    return fail(MUON_ERR_ALIGNMENT, who + what + ": codes and their leading dimension are multiples of 16, scales of 4");
+  const uintptr_t c = reinterpret_cast<uintptr_t>(codes), e = reinterpret_cast<uintptr_t>(scales);
+  spans.push_back({c, c + uintptr_t((lines - 1) * ld_codes + blocks * 16), written, matrix, "codes"});
+  spans.push_back({e, e + uintptr_t((lines - 1) * ld_scales + blocks), written, matrix, "scales"});
+  return MUON_OK;
+}
+
+// Checks a list and cuts it into launches.  axis -1: quantising (both forms, where given); else the form read.
+muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vector<Mx4Launch>& out) {
+  if (n < 0) return fail(MUON_ERR_BAD_ARG, "n < 0");
+  if (n > 0 && !list) return fail(MUON_ERR_NULL_ARG, "list is NULL");
+  const bool quantize = axis < 0;
+  std::vector<Mx4Span> spans;
+  spans.reserve(size_t(n) * 5);
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_mx4_t& x = list[i];
+    const std::string who = "matrix " + std::to_string(i) + ": ";
+    if (!x.values) return fail(MUON_ERR_NULL_ARG, who + "values is NULL");
+    if (x.dtype != MUON_F32 && x.dtype != MUON_BF16) return fail(MUON_ERR_BAD_DTYPE, who + "dtype must be MUON_F32 or MUON_BF16");
+    constexpr int64_t most = int64_t(1) << 30;
+    if (x.rows < 1 || x.cols < 1 || x.rows > most || x.cols > most)
+      return fail(MUON_ERR_BAD_SHAPE, who + "rows and cols must be in [1, 2^30]");
+    if (x.ld < x.cols) return fail(MUON_ERR_BAD_SHAPE, who + "the leading dimension must be >= cols");
+    if (x.reserved != 0) return fail(MUON_ERR_BAD_ARG, who + "reserved must be 0");
+    const size_t es = x.dtype == MUON_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail(MUON_ERR_ALIGNMENT, who + "values misaligned");
+    const bool row = axis != 0 && (x.row_codes || x.row_scales || axis == 1);
+    const bool col = axis != 1 && (x.col_codes || x.col_scales || axis == 0);
+    if (!row && !col) return fail(MUON_ERR_NULL_ARG, who + "no form is given");
+    muon_status_t st = MUON_OK;
+    if (row) st = check_mx4_form(who, "form along the rows", x.row_codes, x.row_scales, x.ld_row_codes, x.ld_row_scales,
+                                 x.rows, x.cols, quantize, i, spans);
+    if (st == MUON_OK && col)
+      st = check_mx4_form(who, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales,
+                          x.cols, x.rows, quantize, i, spans);
+    if (st != MUON_OK) return st;
+    const uintptr_t v = reinterpret_cast<uintptr_t>(x.values);
+    spans.push_back({v, v + uintptr_t((x.rows - 1) * x.ld + x.cols) * es, !quantize, i, "values"});
+    const bool f32 = x.dtype == MUON_F32;
+    Mx4Dev d;
+    std::memset(&d, 0, sizeof(d));
+    d.values = x.values;
+    d.ld = x.ld;
+    d.rows = int32_t(x.rows);
+    d.cols = int32_t(x.cols);
+    d.index = uint32_t(i);
+    d.vec = v % 16 == 0 && (x.rows == 1 || (x.ld * int64_t(es)) % 16 == 0);
+    d.tiles_c = int32_t((x.cols + kMx4Tile - 1) / kMx4Tile);
+    if (row) {
+      d.row = {x.row_codes, x.row_scales};
+      d.row_ld16 = uint32_t(x.ld_row_codes / 16);
+      d.row_ld4 = uint32_t(x.ld_row_scales / 4);
+    }
+    if (col) {
+      d.col = {x.col_codes, x.col_scales};
+      d.col_ld16 = uint32_t(x.ld_col_codes / 16);
+      d.col_ld4 = uint32_t(x.ld_col_scales / 4);
+    }
+    const int64_t tiles = (x.rows + kMx4Tile - 1) / kMx4Tile * d.tiles_c;
+    if (tiles > kMx4MaxTiles) return fail(MUON_ERR_UNSUPPORTED, who + "more than 2^24 - 1 tiles of 128 x 128");
+    Mx4Launch* to = nullptr;    // the latest launch of this kind, if it has room
+    for (Mx4Launch& k : out)
+      if (k.f32 == f32 && k.row == row && k.col == col) to = &k;
+    if (!to || to->list.n == kMx4Most || to->list.tiles + tiles > kMx4MaxTiles) {
+      out.emplace_back();
+      to = &out.back();
+      to->f32 = f32;
+      to->row = row;
+      to->col = col;
+      to->list.n = to->list.tiles = 0;
+    }
+    d.tile0 = to->list.tiles;
+    to->list.m[to->list.n++] = d;
+    to->list.tiles += int32_t(tiles);
+  }
+  // what is written overlaps nothing; what is read may be read twice
+  std::sort(spans.begin(), spans.end(), [](const Mx4Span& a, const Mx4Span& b) { return a.lo < b.lo; });
+  const Mx4Span *any = nullptr, *written = nullptr;     // of those before, the ones that end last
+  for (const Mx4Span& x : spans) {
+    const Mx4Span* const hit = x.written ? any : written;
+    if (hit && x.lo < hit->hi)
+      return fail(MUON_ERR_ALIASING, std::string("buffers overlap: matrix ") + std::to_string(hit->matrix) + " " + hit->what +
+                                         " and matrix " + std::to_string(x.matrix) + " " + x.what);
+    if (!any || x.hi > any->hi) any = &x;
+    if (x.written && (!written || x.hi > written->hi)) written = &x;
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+
 struct muon_handle_s {
   Plan plan;
   muon_hparams_t hp;
@@ -862,6 +973,7 @@ struct muon_handle_s {
   float max_norm = 0.f;          // > 0: every step clips by the global gradient norm
   float* norm_out = nullptr;     // where the caller wants the norm and the factor, or NULL
   uint64_t rounding_seed = 0;
+  std::vector<Mx4Launch> mx4_weights;   // 4-bit copies of the weights, renewed by every step
   int static_device = -1;        // muon_init_static: the GPU whose scratch array holds the workspace
   uint64_t static_generation = 0;  // ... and which of its static inits this handle is
 
@@ -880,8 +992,9 @@ struct muon_handle_s {
 
 namespace {
 
-// Phases of the gradient norm, before the others.
+// Phases of the gradient norm, before the others, and of the weights' 4-bit copies, behind them.
 int32_t norm_phases(muon_handle_t h) { return h->max_norm > 0.f ? 1 : 0; }
+int32_t mx4_phases(muon_handle_t h) { return h->mx4_weights.empty() ? 0 : 1; }
 
 // Enqueue one whole step.  With `ev` non-null, record ev[k] before launch k
 // and ev[last] after the final one.
@@ -1017,6 +1130,14 @@ muon_status_t enqueue_step(muon_handle_t h, float lr, hipStream_t s, std::vector
     if (h->aux_stream && (hipEventRecord(h->ev_aux, h->aux_stream) != hipSuccess ||
                           hipStreamWaitEvent(s, h->ev_aux, 0) != hipSuccess))
       return fail(MUON_ERR_HIP, "lane join failed");
+  }
+  if (!h->mx4_weights.empty()) {
+    Range r("muon.mx4_weights");
+    for (const Mx4Launch& k : h->mx4_weights) {
+      const hipError_t e = launch_mx4_quantize(k.list, k.f32, /*random=*/false, RoundingSeed{0, 0}, s);
+      if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("mx4 weights launch: ") + hipGetErrorString(e));
+    }
+    if (!mark()) return fail(MUON_ERR_HIP, "hipEventRecord failed");
   }
   h->last_stream = s;
   return MUON_OK;
@@ -1472,6 +1593,74 @@ muon_status_t muon_precond_refresh(muon_handle_t h, int32_t slot, int32_t block,
   });
 }
 
+namespace {
+
+// Activations in 4 bits: a line for each feature, in blocks along n_rows samples.
+muon_status_t check_mx4_acts(const Mx4Acts& a) {
+  if (!a.codes || !a.scales) return fail(MUON_ERR_NULL_ARG, "activations are NULL");
+  const int64_t blocks = a.n_rows / kMx4Block + (a.n_rows % kMx4Block != 0);
+  if (a.n_rows < 1 || a.n_rows > int64_t(1) << 30 || a.ld_codes < blocks * 16 || a.ld_scales < blocks)
+    return fail(MUON_ERR_BAD_SHAPE, "activations need 1 <= n_rows <= 2^30 and leading dimensions of a line's blocks");
+  if (reinterpret_cast<uintptr_t>(a.codes) % 16 || a.ld_codes % 16 || reinterpret_cast<uintptr_t>(a.scales) % 4 ||
+      a.ld_scales % 4)
+    return fail(MUON_ERR_ALIGNMENT, "codes and their leading dimension are multiples of 16, scales of 4");
+  return MUON_OK;
+}
+
+}  // namespace
+
+muon_status_t muon_precond_accumulate_mx4(muon_handle_t h, int32_t slot, int32_t block, const uint8_t* codes,
+                                          const uint8_t* scales, int64_t n_rows, int64_t ld_codes, int64_t ld_scales,
+                                          double beta, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    const SlotPlan& sp = h->plan.slots[size_t(slot)];
+    const Mx4Acts acts{codes, scales, ld_codes, ld_scales, n_rows};
+    if ((st = check_mx4_acts(acts)) != MUON_OK) return st;
+    if (!(beta >= 0.0 && beta <= 1.0)) return fail(MUON_ERR_BAD_ARG, "beta must be in [0, 1]");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Range r("muon.precond_accumulate");
+    const hipError_t e = launch_precond_accumulate_mx4(block_dev(h, sp, block), acts, beta, s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond accumulate launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_precond_refresh_mx4(muon_handle_t h, int32_t slot, int32_t block, const uint8_t* codes,
+                                       const uint8_t* scales, int64_t n_rows, int64_t ld_codes, int64_t ld_scales,
+                                       float damping, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    const SlotPlan& sp = h->plan.slots[size_t(slot)];
+    const Mx4Acts acts{codes, scales, ld_codes, ld_scales, n_rows};
+    if ((st = check_mx4_acts(acts)) != MUON_OK) return st;
+    if (!std::isfinite(damping) || damping < 0.f) return fail(MUON_ERR_BAD_ARG, "damping must be finite and >= 0");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    Range r("muon.precond_refresh");
+    const hipError_t e = launch_precond_refresh_mx4(block_dev(h, sp, block), acts, damping,
+                                                    reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
+    if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond refresh launch: ") + hipGetErrorString(e));
+    h->last_stream = s;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_precond_sums(muon_handle_t h, int32_t slot, int32_t block, float** sums, int64_t* ld, double** count) {
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_slot_block(h, slot, block);
+    if (st != MUON_OK) return st;
+    const SlotPlan& sp = h->plan.slots[size_t(slot)];
+    const PrecondBlockDev b = block_dev(h, sp, block);
+    if (sums) *sums = b.acc;
+    if (ld) *ld = sp.dp;
+    if (count) *count = b.cnt;
+    return MUON_OK;
+  });
+}
+
 muon_status_t muon_step(muon_handle_t h, float lr, void* stream) {
   return guarded([&]() -> muon_status_t {
     if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
@@ -1487,7 +1676,7 @@ muon_status_t muon_step_timed(muon_handle_t h, float lr, void* stream, float* ph
     if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
     if (!std::isfinite(lr)) return fail(MUON_ERR_BAD_ARG, "lr is not finite");
     if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
-    const size_t np = size_t(norm_phases(h)) + h->phase_names.size();
+    const size_t np = size_t(norm_phases(h)) + h->phase_names.size() + size_t(mx4_phases(h));
     h->events.reserve(np + 1);
     while (h->events.size() < np + 1) {
       hipEvent_t ev;
@@ -1514,6 +1703,7 @@ const char* muon_phase_name(muon_handle_t h, int32_t phase) {
   if (!h || phase < 0) return "";
   if (phase < norm_phases(h)) return "grad_norm";
   const size_t k = size_t(phase - norm_phases(h));
+  if (k == h->phase_names.size() && mx4_phases(h)) return "mx4_weights";
   return k < h->phase_names.size() ? h->phase_names[k].c_str() : "";
 }
 
@@ -1573,6 +1763,36 @@ muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* nor
   });
 }
 
+muon_status_t muon_set_mx4_weights(muon_handle_t h, const muon_mx4_t* copies, int32_t n) {
+  return guarded([&]() -> muon_status_t {
+    if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    std::vector<Mx4Launch> launches;
+    muon_status_t st = mx4_launches(copies, n, -1, launches);
+    if (st != MUON_OK) return st;
+    for (int32_t i = 0; i < n; ++i) {
+      const muon_mx4_t& x = copies[i];
+      const auto is_param = [&](const muon_tensor_t& t) {
+        return t.param == x.values && t.rows == x.rows && t.cols == x.cols && t.ld_param == x.ld && t.dtype == x.dtype;
+      };
+      if (std::none_of(h->tensors.begin(), h->tensors.end(), is_param))
+        return fail(MUON_ERR_BAD_ARG, "matrix " + std::to_string(i) + ": not the param of a registered tensor");
+      const std::string who = "matrix " + std::to_string(i) + " ";
+      const auto apart = [&](const uint8_t* p, int64_t lines, int64_t ld, int64_t width, const char* what) {
+        if (!p || st != MUON_OK) return;
+        st = check_apart(h, p, size_t((lines - 1) * ld + width), (who + what).c_str());
+      };
+      const int64_t across = (x.cols + kMx4Block - 1) / kMx4Block, down = (x.rows + kMx4Block - 1) / kMx4Block;
+      apart(x.row_codes, x.rows, x.ld_row_codes, across * 16, "codes");
+      apart(x.row_scales, x.rows, x.ld_row_scales, across, "scales");
+      apart(x.col_codes, x.cols, x.ld_col_codes, down * 16, "codes");
+      apart(x.col_scales, x.cols, x.ld_col_scales, down, "scales");
+      if (st != MUON_OK) return st;
+    }
+    h->mx4_weights = std::move(launches);
+    return MUON_OK;
+  });
+}
+
 muon_status_t muon_pack_moments(muon_handle_t h, const void* values, int32_t dtype, void* stream) {
   return guarded([&]() -> muon_status_t {
     muon_status_t st = check_values(h, values, dtype);
@@ -1608,119 +1828,6 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
     return MUON_OK;
   });
 }
-
-namespace {
-
-// One launch over matrices of one dtype and one choice of forms.
-struct Mx4Launch {
-  Mx4List list;
-  bool f32, row, col;
-};
-
-// A span of memory that a call on a list touches.
-struct Mx4Span { uintptr_t lo, hi; bool written; int32_t matrix; const char* what; };
-
-// One form's lines: their addresses, alignment and span.
-muon_status_t check_mx4_form(const std::string& who, const char* what, const uint8_t* codes, const uint8_t* scales,
-                             int64_t ld_codes, int64_t ld_scales, int64_t lines, int64_t length, bool written,
-                             int32_t matrix, std::vector<Mx4Span>& spans) {
-  if (!codes || !scales) return fail(MUON_ERR_NULL_ARG, who + what + ": codes and scales go together");
-  const int64_t blocks = (length + kMx4Block - 1) / kMx4Block;
-  if (ld_codes < blocks * 16 || ld_scales < blocks)
-    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions below a line's blocks");
-  if (ld_codes > int64_t(16) << 31 || ld_scales > int64_t(4) << 31)
-    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions too large");
-  if (reinterpret_cast<uintptr_t>(codes) % 16 || ld_codes % 16 || reinterpret_cast<uintptr_t>(scales) % 4 || ld_scales % 4)
-    return fail(MUON_ERR_ALIGNMENT, who + what + ": codes and their leading dimension are multiples of 16, scales of 4");
-  const uintptr_t c = reinterpret_cast<uintptr_t>(codes), e = reinterpret_cast<uintptr_t>(scales);
-  spans.push_back({c, c + uintptr_t((lines - 1) * ld_codes + blocks * 16), written, matrix, "codes"});
-  spans.push_back({e, e + uintptr_t((lines - 1) * ld_scales + blocks), written, matrix, "scales"});
-  return MUON_OK;
-}
-
-// Checks a list and cuts it into launches.  axis -1: quantising (both forms, where given); else the form read.
-muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vector<Mx4Launch>& out) {
-  if (n < 0) return fail(MUON_ERR_BAD_ARG, "n < 0");
-  if (n > 0 && !list) return fail(MUON_ERR_NULL_ARG, "list is NULL");
-  const bool quantize = axis < 0;
-  std::vector<Mx4Span> spans;
-  spans.reserve(size_t(n) * 5);
-  for (int32_t i = 0; i < n; ++i) {
-    const muon_mx4_t& x = list[i];
-    const std::string who = "matrix " + std::to_string(i) + ": ";
-    if (!x.values) return fail(MUON_ERR_NULL_ARG, who + "values is NULL");
-    if (x.dtype != MUON_F32 && x.dtype != MUON_BF16) return fail(MUON_ERR_BAD_DTYPE, who + "dtype must be MUON_F32 or MUON_BF16");
-    constexpr int64_t most = int64_t(1) << 30;
-    if (x.rows < 1 || x.cols < 1 || x.rows > most || x.cols > most)
-      return fail(MUON_ERR_BAD_SHAPE, who + "rows and cols must be in [1, 2^30]");
-    if (x.ld < x.cols) return fail(MUON_ERR_BAD_SHAPE, who + "the leading dimension must be >= cols");
-    if (x.reserved != 0) return fail(MUON_ERR_BAD_ARG, who + "reserved must be 0");
-    const size_t es = x.dtype == MUON_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail(MUON_ERR_ALIGNMENT, who + "values misaligned");
-    const bool row = axis != 0 && (x.row_codes || x.row_scales || axis == 1);
-    const bool col = axis != 1 && (x.col_codes || x.col_scales || axis == 0);
-    if (!row && !col) return fail(MUON_ERR_NULL_ARG, who + "no form is given");
-    muon_status_t st = MUON_OK;
-    if (row) st = check_mx4_form(who, "form along the rows", x.row_codes, x.row_scales, x.ld_row_codes, x.ld_row_scales,
-                                 x.rows, x.cols, quantize, i, spans);
-    if (st == MUON_OK && col)
-      st = check_mx4_form(who, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales,
-                          x.cols, x.rows, quantize, i, spans);
-    if (st != MUON_OK) return st;
-    const uintptr_t v = reinterpret_cast<uintptr_t>(x.values);
-    spans.push_back({v, v + uintptr_t((x.rows - 1) * x.ld + x.cols) * es, !quantize, i, "values"});
-    const bool f32 = x.dtype == MUON_F32;
-    Mx4Dev d;
-    std::memset(&d, 0, sizeof(d));
-    d.values = x.values;
-    d.ld = x.ld;
-    d.rows = int32_t(x.rows);
-    d.cols = int32_t(x.cols);
-    d.index = uint32_t(i);
-    d.vec = v % 16 == 0 && (x.rows == 1 || (x.ld * int64_t(es)) % 16 == 0);
-    d.tiles_c = int32_t((x.cols + kMx4Tile - 1) / kMx4Tile);
-    if (row) {
-      d.row = {x.row_codes, x.row_scales};
-      d.row_ld16 = uint32_t(x.ld_row_codes / 16);
-      d.row_ld4 = uint32_t(x.ld_row_scales / 4);
-    }
-    if (col) {
-      d.col = {x.col_codes, x.col_scales};
-      d.col_ld16 = uint32_t(x.ld_col_codes / 16);
-      d.col_ld4 = uint32_t(x.ld_col_scales / 4);
-    }
-    const int64_t tiles = (x.rows + kMx4Tile - 1) / kMx4Tile * d.tiles_c;
-    if (tiles > kMx4MaxTiles) return fail(MUON_ERR_UNSUPPORTED, who + "more than 2^24 - 1 tiles of 128 x 128");
-    Mx4Launch* to = nullptr;    // the latest launch of this kind, if it has room
-    for (Mx4Launch& k : out)
-      if (k.f32 == f32 && k.row == row && k.col == col) to = &k;
-    if (!to || to->list.n == kMx4Most || to->list.tiles + tiles > kMx4MaxTiles) {
-      out.emplace_back();
-      to = &out.back();
-      to->f32 = f32;
-      to->row = row;
-      to->col = col;
-      to->list.n = to->list.tiles = 0;
-    }
-    d.tile0 = to->list.tiles;
-    to->list.m[to->list.n++] = d;
-    to->list.tiles += int32_t(tiles);
-  }
-  // what is written overlaps nothing; what is read may be read twice
-  std::sort(spans.begin(), spans.end(), [](const Mx4Span& a, const Mx4Span& b) { return a.lo < b.lo; });
-  const Mx4Span *any = nullptr, *written = nullptr;     // of those before, the ones that end last
-  for (const Mx4Span& x : spans) {
-    const Mx4Span* const hit = x.written ? any : written;
-    if (hit && x.lo < hit->hi)
-      return fail(MUON_ERR_ALIASING, std::string("buffers overlap: matrix ") + std::to_string(hit->matrix) + " " + hit->what +
-                                         " and matrix " + std::to_string(x.matrix) + " " + x.what);
-    if (!any || x.hi > any->hi) any = &x;
-    if (x.written && (!written || x.hi > written->hi)) written = &x;
-  }
-  return MUON_OK;
-}
-
-}  // namespace
 
 muon_status_t muon_mx4_quantize(const muon_mx4_t* list, int32_t n, int32_t rounding, uint64_t seed, void* stream) {
   return guarded([&]() -> muon_status_t {

@@ -249,6 +249,26 @@ struct Mx4Dev {
 struct Mx4List { Mx4Dev m[kMx4Most]; int32_t n, tiles; };
 static_assert(sizeof(Mx4List) + 64 <= 4096, "kernel arguments");
 
+// Activations held so, and what their second moment goes to: one line of codes
+// and scales a feature, in blocks along the samples.
+struct Mx4Acts {
+  const uint8_t* codes; const uint8_t* scales;
+  int64_t ld_codes, ld_scales;         // bytes
+  int64_t n_rows;                      // samples
+};
+struct Mx4MomentParams {
+  const uint8_t* codes; const uint8_t* scales;
+  int64_t ld_codes, ld_scales, n_rows;
+  int32_t d, dp;
+  float* out;                          // S or the running sums, dp x dp
+  float inv_n, damping;                // S = X^T X * inv_n + damping * I ...
+  int32_t accumulate;
+  double beta;                         // ... or, accumulating, sums = beta * sums + X^T X
+  double* cnt;                         // NULL, or the running count: beta * count + n_rows
+  float* part;                         // partial sums of ranges of samples, or NULL
+  int64_t stages;                      // of a range
+};
+
 // Global gradient norm: every registered gradient as a run of n elements cut
 // in chunks of kNormChunk, the chunks of all tensors numbered through; block b
 // of n sums chunks b, b + n and so on.
@@ -293,6 +313,11 @@ hipError_t launch_precond_accumulate(const PrecondBlockDev& b, const void* acts,
 hipError_t launch_precond_refresh_accumulated(const PrecondBlockDev& b, float damping, bool reset, uint32_t* flags,
                                               hipStream_t s);
 // tasks: n_bf16 tiles of bf16-gradient tensors, then n_f32 of float32 ones
+// floats that the scratch of a block's partial sums holds at the least
+inline size_t moment_part_floats(int dp) {
+  const size_t sq = size_t(dp) * dp, splits = size_t(moment_splits(dp, false, INT64_MAX));
+  return sq * (splits > 2 ? splits : 2);
+}
 hipError_t launch_precond_apply(const PrecondDev* pds, const ApplyTask* tasks, int n_bf16, int n_f32, hipStream_t s);
 hipError_t launch_identity(uint16_t* sinv, int dp, int nblocks, hipStream_t s);
 hipError_t launch_adam_tick(AdamState* st, float beta1, float beta2, hipStream_t s);
@@ -321,6 +346,12 @@ MUON_WEAK hipError_t launch_unpack_moments(const PackedDev* tensors, const Packe
                                            void* values, int64_t n_values, bool f32, uint32_t* flags,
                                            hipStream_t s);
 MUON_WEAK hipError_t launch_grad_norm(const NormParams& p, hipStream_t s);
+// part_floats: what p.part holds
+MUON_WEAK hipError_t launch_mx4_moment(Mx4MomentParams p, size_t part_floats, hipStream_t s);
+MUON_WEAK hipError_t launch_precond_refresh_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, float damping,
+                                                uint32_t* flags, hipStream_t s);
+MUON_WEAK hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, double beta,
+                                                   hipStream_t s);
 // the matrices of a list share dtype and forms; axis: 1 the form along the rows is read, 0 along the columns
 MUON_WEAK hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, RoundingSeed seed, hipStream_t s);
 MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, hipStream_t s);

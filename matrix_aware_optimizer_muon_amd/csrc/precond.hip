@@ -1054,6 +1054,41 @@ hipError_t launch_precond_refresh_accumulated(const PrecondBlockDev& b, float da
   return hipGetLastError();
 }
 
+namespace {
+Mx4MomentParams mx4_params(const PrecondBlockDev& b, const Mx4Acts& acts, float* out) {
+  Mx4MomentParams p = {};
+  p.codes = acts.codes;
+  p.scales = acts.scales;
+  p.ld_codes = acts.ld_codes;
+  p.ld_scales = acts.ld_scales;
+  p.n_rows = acts.n_rows;
+  p.d = b.d;
+  p.dp = b.dp;
+  p.out = out;
+  p.part = b.part;
+  return p;
+}
+}  // namespace
+
+hipError_t launch_precond_refresh_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, float damping, uint32_t* flags,
+                                      hipStream_t s) {
+  Mx4MomentParams p = mx4_params(b, acts, b.s);
+  p.inv_n = static_cast<float>(1.0 / static_cast<double>(acts.n_rows));
+  p.damping = damping;
+  const hipError_t e = launch_mx4_moment(p, moment_part_floats(b.dp), s);
+  if (e != hipSuccess) return e;
+  factor_and_invert(b, flags, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, double beta, hipStream_t s) {
+  Mx4MomentParams p = mx4_params(b, acts, b.acc);
+  p.accumulate = 1;
+  p.beta = beta;
+  p.cnt = b.cnt;
+  return launch_mx4_moment(p, moment_part_floats(b.dp), s);
+}
+
 hipError_t launch_precond_apply(const PrecondDev* pds, const ApplyTask* tasks, int n_bf16, int n_f32, hipStream_t s) {
   if (n_bf16 > 0) apply_kernel<false><<<n_bf16, kThreads, 0, s>>>(pds, tasks);
   if (n_f32 > 0) apply_kernel<true><<<n_f32, kThreads, 0, s>>>(pds, tasks + n_bf16);
