@@ -238,7 +238,7 @@ muon_status_t muon_precond_refresh_accumulated(muon_handle_t h, int32_t slot, in
 /* Both calls for activations held in microscaled 4-bit floats (below) with
  * blocks along the samples, the form along the columns of the n_rows x d
  * activations: line i of codes and scales is feature i, ld_codes and ld_scales
- * bytes from the next; n_rows in [1, 2^30].  Otherwise as
+ * bytes (at most 2^24 each) from the next.  Otherwise as
  * muon_precond_refresh and muon_precond_accumulate, but for beta in float64:
  * Sigma and N are decayed by the same factor, in float64, Sigma then rounded.
  * The products are exact in float32 and summed in it.  What lies behind the n_rows-th sample of a line is

@@ -1599,8 +1599,10 @@ namespace {
 muon_status_t check_mx4_acts(const Mx4Acts& a) {
   if (!a.codes || !a.scales) return fail(MUON_ERR_NULL_ARG, "activations are NULL");
   const int64_t blocks = a.n_rows / kMx4Block + (a.n_rows % kMx4Block != 0);
-  if (a.n_rows < 1 || a.n_rows > int64_t(1) << 30 || a.ld_codes < blocks * 16 || a.ld_scales < blocks)
-    return fail(MUON_ERR_BAD_SHAPE, "activations need 1 <= n_rows <= 2^30 and leading dimensions of a line's blocks");
+  if (a.n_rows < 1 || a.ld_codes < blocks * 16 || a.ld_scales < blocks)
+    return fail(MUON_ERR_BAD_SHAPE, "activations need n_rows >= 1 and leading dimensions of a line's blocks");
+  if (a.ld_codes > int64_t(1) << 24 || a.ld_scales > int64_t(1) << 24)   // a tile's offsets have 32 bits
+    return fail(MUON_ERR_UNSUPPORTED, "leading dimensions of activations above 2^24 bytes");
   if (reinterpret_cast<uintptr_t>(a.codes) % 16 || a.ld_codes % 16 || reinterpret_cast<uintptr_t>(a.scales) % 4 ||
       a.ld_scales % 4)
     return fail(MUON_ERR_ALIGNMENT, "codes and their leading dimension are multiples of 16, scales of 4");
@@ -1621,7 +1623,8 @@ muon_status_t muon_precond_accumulate_mx4(muon_handle_t h, int32_t slot, int32_t
     if (!(beta >= 0.0 && beta <= 1.0)) return fail(MUON_ERR_BAD_ARG, "beta must be in [0, 1]");
     hipStream_t s = static_cast<hipStream_t>(stream);
     Range r("muon.precond_accumulate");
-    const hipError_t e = launch_precond_accumulate_mx4(block_dev(h, sp, block), acts, beta, s);
+    const hipError_t e = launch_precond_accumulate_mx4(
+        block_dev(h, sp, block), acts, beta, reinterpret_cast<uint32_t*>(h->ws + h->plan.off_flags), s);
     if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("precond accumulate launch: ") + hipGetErrorString(e));
     h->last_stream = s;
     return MUON_OK;

@@ -265,8 +265,10 @@ struct Mx4MomentParams {
   int32_t accumulate;
   double beta;                         // ... or, accumulating, sums = beta * sums + X^T X
   double* cnt;                         // NULL, or the running count: beta * count + n_rows
-  float* part;                         // partial sums of ranges of samples, or NULL
-  int64_t stages;                      // of a range
+  float* part;                         // room for partial sums of ranges of samples, or NULL
+  size_t part_floats;
+  int32_t whole, splits, stages;       // of the launch: tiles taken whole, ranges of each other one, stages of a range
+  uint32_t* flags;                     // the handle's flag word (bounds checks of a debug build)
 };
 
 // Global gradient norm: every registered gradient as a run of n elements cut
@@ -346,12 +348,11 @@ MUON_WEAK hipError_t launch_unpack_moments(const PackedDev* tensors, const Packe
                                            void* values, int64_t n_values, bool f32, uint32_t* flags,
                                            hipStream_t s);
 MUON_WEAK hipError_t launch_grad_norm(const NormParams& p, hipStream_t s);
-// part_floats: what p.part holds
-MUON_WEAK hipError_t launch_mx4_moment(Mx4MomentParams p, size_t part_floats, hipStream_t s);
+MUON_WEAK hipError_t launch_mx4_moment(Mx4MomentParams p, hipStream_t s);
 MUON_WEAK hipError_t launch_precond_refresh_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, float damping,
                                                 uint32_t* flags, hipStream_t s);
 MUON_WEAK hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, double beta,
-                                                   hipStream_t s);
+                                                   uint32_t* flags, hipStream_t s);
 // the matrices of a list share dtype and forms; axis: 1 the form along the rows is read, 0 along the columns
 MUON_WEAK hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, RoundingSeed seed, hipStream_t s);
 MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, hipStream_t s);

@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "lds_ring.h"
 #include "muon_internal.h"
 
 namespace muon {
@@ -116,26 +117,6 @@ __device__ __forceinline__ int swz_kc(int r, int c) {
 }
 __device__ __forceinline__ int swz_km(int k, int c) { return c ^ ((k & 3) << 2); }
 
-// Wait until at most N vector-memory operations of this wave are pending
-// (asm, so the compiler, which does not see the asm loads, keeps it).
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// Workgroup barrier for the stage ring.  A __syncthreads fence would also
-// wait for every direct-to-LDS load in flight (they count as LDS writes)
-// and drain the ring; here each wave only completes its own LDS reads
-// (lgkmcnt(0): the buffer refilled after the barrier was read before it),
-// and callers wait for the loads they need with wait_vmcnt.  The asm
-// memory clobbers keep the compiler from moving memory accesses across.
-__device__ __forceinline__ void ring_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Orders one wave's LDS writes before its other lanes read them back (the
 // epilogue's staging area is private to the wave): a release and an acquire
 // fence at wavefront scope around a wave barrier, so neither the compiler
@@ -162,19 +143,8 @@ __device__ __forceinline__ bf16x4_t lds_read_tr(const uint16_t* p) {
 // lands NW*64 chunks further, a whole number of rows whose swizzle repeats,
 // so its global chunk is the same offset from a base advanced by astep /
 // bstep bytes (one VGPR per operand instead of one per instruction).  No
-// VGPR holds the data and no LDS store instruction is issued.
-//
-// The instruction is written as inline asm (it has no register result): the
-// compiler treats the builtin form as an LDS store and puts a wait for every
-// outstanding vector-memory operation in front of the next LDS read, which
-// would drain the ring.  The stage waits are therefore explicit
-// (wait_vmcnt), and the asm's memory clobber keeps LDS accesses in order
-// around it.
-__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
-               : "memory", "m0");
-}
-
+// VGPR holds the data and no LDS store instruction is issued (dma16,
+// lds_ring.h).
 template <int NA, int NB, int NW, typename E>
 __device__ __forceinline__ void issue_stage(const E* ga, const E* gb, uint32_t aoff, uint32_t boff, size_t astep,
                                             size_t bstep, uint32_t la, uint32_t lb, int wave, bool with_b) {
@@ -186,12 +156,6 @@ __device__ __forceinline__ void issue_stage(const E* ga, const E* gb, uint32_t a
     for (int i = 0; i < NB; ++i)
       dma16(reinterpret_cast<const char*>(gb) + i * bstep, boff, lb + (i * NW + wave) * 1024);
   }
-}
-
-// LDS byte address of a shared-memory pointer.
-template <typename E>
-__device__ __forceinline__ uint32_t lds_addr(const E* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const E*)(p)));
 }
 
 // The lane's index in its wave, from the lane masks rather than the thread

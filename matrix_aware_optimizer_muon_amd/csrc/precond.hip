@@ -1055,7 +1055,7 @@ hipError_t launch_precond_refresh_accumulated(const PrecondBlockDev& b, float da
 }
 
 namespace {
-Mx4MomentParams mx4_params(const PrecondBlockDev& b, const Mx4Acts& acts, float* out) {
+Mx4MomentParams mx4_params(const PrecondBlockDev& b, const Mx4Acts& acts, float* out, uint32_t* flags) {
   Mx4MomentParams p = {};
   p.codes = acts.codes;
   p.scales = acts.scales;
@@ -1066,27 +1066,30 @@ Mx4MomentParams mx4_params(const PrecondBlockDev& b, const Mx4Acts& acts, float*
   p.dp = b.dp;
   p.out = out;
   p.part = b.part;
+  p.part_floats = b.part ? moment_part_floats(b.dp) : 0;
+  p.flags = flags;
   return p;
 }
 }  // namespace
 
 hipError_t launch_precond_refresh_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, float damping, uint32_t* flags,
                                       hipStream_t s) {
-  Mx4MomentParams p = mx4_params(b, acts, b.s);
+  Mx4MomentParams p = mx4_params(b, acts, b.s, flags);
   p.inv_n = static_cast<float>(1.0 / static_cast<double>(acts.n_rows));
   p.damping = damping;
-  const hipError_t e = launch_mx4_moment(p, moment_part_floats(b.dp), s);
+  const hipError_t e = launch_mx4_moment(p, s);
   if (e != hipSuccess) return e;
   factor_and_invert(b, flags, s);
   return hipGetLastError();
 }
 
-hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, double beta, hipStream_t s) {
-  Mx4MomentParams p = mx4_params(b, acts, b.acc);
+hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, const Mx4Acts& acts, double beta, uint32_t* flags,
+                                         hipStream_t s) {
+  Mx4MomentParams p = mx4_params(b, acts, b.acc, flags);
   p.accumulate = 1;
   p.beta = beta;
   p.cnt = b.cnt;
-  return launch_mx4_moment(p, moment_part_floats(b.dp), s);
+  return launch_mx4_moment(p, s);
 }
 
 hipError_t launch_precond_apply(const PrecondDev* pds, const ApplyTask* tasks, int n_bf16, int n_f32, hipStream_t s) {

@@ -84,7 +84,30 @@ def test_sums_are_exact(n, d):
     opt.close()
 
 
-@pytest.mark.parametrize("n,d", [(100, 64), (5003, 300), (40000, 129), (65536, 768)])
+@pytest.mark.parametrize("n,d", [(511, 1300), (512, 1300), (513, 1300), (600, 1153), (767, 1281), (768, 1600), (800, 2000),
+                                 (1023, 1153), (1024, 1200), (1025, 1400), (1536, 1100), (1600, 500), (1792, 130),
+                                 (2303, 1290), (2816, 40), (5120, 1025), (7000, 3), (9999, 2700), (34309, 2100),
+                                 (34560, 2100), (100001, 2049)])
+def test_sums_are_exact_in_every_way(n, d):
+    """Bands and tiles of both sizes, whole and cut, with every length of the last stage's kind.  Scales of 1: products
+    are multiples of 1/4 up to 36, exact for 116508 samples."""
+    say(f"case: sums of {n} samples, {d} features")
+    opt = handle(d)
+    sums, count = opt.precond_sums(0, 0)
+    q = held(n, d, scales=(127, 128), wide=1)
+    x = decoded(q)
+    want = x @ x.t().contiguous()
+    for beta in (0.0, 1.0):
+        sums.fill_(3.0 if beta else float("nan"))
+        count.fill_(7.0)
+        opt.precond_accumulate(0, 0, q, beta=beta)
+        assert torch.equal(sums.double(), want + 3.0 * beta) and float(count) == n + 7.0 * beta
+        assert not any(bool(p.any()) for p in padding(opt, d))
+    assert opt.flags() == 0
+    opt.close()
+
+
+@pytest.mark.parametrize("n,d", [(100, 64), (5003, 300), (40000, 129), (65536, 768), (40000, 2100)])
 def test_sums_with_scales_of_any_size(n, d):
     say(f"case: sums of {n} samples, {d} features, scales 2^-20 .. 2^20")
     opt = handle(d)
