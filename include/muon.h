@@ -384,7 +384,7 @@ typedef struct {
 } muon_mx4_t;
 
 /* Rounds each matrix of the list to the forms it names (at least one), both from
- * one read; one launch for up to 44 matrices of one dtype and one choice of
+ * one read; one launch for up to 64 matrices of one dtype and one choice of
  * forms.  Needs no handle; works on the calling thread's current device,
  * asynchronous on `stream`.  The forms' spans must not overlap each other or any
  * values of the list.  `seed` is of use only for MUON_ROUND_RANDOM. */

@@ -847,7 +847,7 @@ namespace {
 // One launch over matrices of one dtype and one choice of forms.
 struct Mx4Launch {
   Mx4List list;
-  bool f32, row, col;
+  bool f32, row, col, stream;
 };
 
 // A span of memory that a call on a list touches.
@@ -871,11 +871,26 @@ muon_status_t check_mx4_form(const std::string& who, const char* what, const uin
   return MUON_OK;
 }
 
+// Whether every row of values begins at a multiple of 16 bytes.
+bool mx4_aligned(const muon_mx4_t& x) {
+  const int64_t es = x.dtype == MUON_F32 ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(x.values) % 16 == 0 && (x.rows == 1 || x.ld % (16 / es) == 0);
+}
+
 // Checks a list and cuts it into launches.  axis -1: quantising (both forms, where given); else the form read.
 muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vector<Mx4Launch>& out) {
   if (n < 0) return fail(MUON_ERR_BAD_ARG, "n < 0");
   if (n > 0 && !list) return fail(MUON_ERR_NULL_ARG, "list is NULL");
   const bool quantize = axis < 0;
+  // Values that are written go past the caches where their rows allow it.  A list that holds both kinds takes two
+  // launches for that, which a small one is not worth.
+  bool all_aligned = true;
+  size_t value_bytes = 0;
+  for (int32_t i = 0; !quantize && i < n; ++i) {
+    all_aligned = all_aligned && mx4_aligned(list[i]);
+    value_bytes += size_t(std::max<int64_t>(list[i].rows, 0)) * size_t(std::max<int64_t>(list[i].cols, 0)) * 4;
+  }
+  const bool stream_where = !quantize && (all_aligned || value_bytes > size_t(64) << 20);
   std::vector<Mx4Span> spans;
   spans.reserve(size_t(n) * 5);
   for (int32_t i = 0; i < n; ++i) {
@@ -910,7 +925,7 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
     d.rows = int32_t(x.rows);
     d.cols = int32_t(x.cols);
     d.index = uint32_t(i);
-    d.vec = v % 16 == 0 && (x.rows == 1 || (x.ld * int64_t(es)) % 16 == 0);
+    const bool streams = stream_where && mx4_aligned(x);
     d.tiles_c = int32_t((x.cols + kMx4Tile - 1) / kMx4Tile);
     if (row) {
       d.row = {x.row_codes, x.row_scales};
@@ -926,16 +941,17 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
     if (tiles > kMx4MaxTiles) return fail(MUON_ERR_UNSUPPORTED, who + "more than 2^24 - 1 tiles of 128 x 128");
     Mx4Launch* to = nullptr;    // the latest launch of this kind, if it has room
     for (Mx4Launch& k : out)
-      if (k.f32 == f32 && k.row == row && k.col == col) to = &k;
+      if (k.f32 == f32 && k.row == row && k.col == col && k.stream == streams) to = &k;
     if (!to || to->list.n == kMx4Most || to->list.tiles + tiles > kMx4MaxTiles) {
       out.emplace_back();
       to = &out.back();
       to->f32 = f32;
       to->row = row;
       to->col = col;
+      to->stream = streams;
       to->list.n = to->list.tiles = 0;
     }
-    d.tile0 = to->list.tiles;
+    to->list.tile0[to->list.n] = to->list.tiles;
     to->list.m[to->list.n++] = d;
     to->list.tiles += int32_t(tiles);
   }
@@ -1856,7 +1872,7 @@ muon_status_t muon_mx4_dequantize(const muon_mx4_t* list, int32_t n, int32_t axi
     if (st != MUON_OK) return st;
     Range r("muon.mx4_dequantize");
     for (const Mx4Launch& k : launches) {
-      const hipError_t e = launch_mx4_dequantize(k.list, k.f32, axis, static_cast<hipStream_t>(stream));
+      const hipError_t e = launch_mx4_dequantize(k.list, k.f32, axis, k.stream, static_cast<hipStream_t>(stream));
       if (e != hipSuccess) return fail(MUON_ERR_HIP, std::string("mx4 dequantize launch: ") + hipGetErrorString(e));
     }
     return MUON_OK;

@@ -234,7 +234,7 @@ struct PackedParams {
 // captured one keeps its list.
 constexpr int kMx4Block = 32;
 constexpr int kMx4Tile = 128;          // a thread block's tile: rows and columns
-constexpr int kMx4Most = 44;           // matrices of a launch: 4 KB of arguments
+constexpr int kMx4Most = 64;           // matrices of a launch, in 6 KB of arguments
 constexpr int64_t kMx4MaxTiles = (int64_t(1) << 24) - 1;   // of a launch: below 2^32 threads
 struct Mx4Form { uint8_t* codes; uint8_t* scales; };
 struct Mx4Dev {
@@ -242,12 +242,15 @@ struct Mx4Dev {
   Mx4Form row, col;
   uint32_t row_ld16, row_ld4, col_ld16, col_ld4;   // of codes in 16 bytes, of scales in 4
   int32_t rows, cols;
-  int32_t tile0, tiles_c;              // tiles of the matrices before this one; tiles across
+  int32_t tiles_c;                     // tiles across
   uint32_t index;                      // its place in the caller's list (random words)
-  int32_t vec;                         // rows of values 16-byte aligned
 };
-struct Mx4List { Mx4Dev m[kMx4Most]; int32_t n, tiles; };
-static_assert(sizeof(Mx4List) + 64 <= 4096, "kernel arguments");
+struct Mx4List {
+  Mx4Dev m[kMx4Most];
+  int32_t tile0[kMx4Most];             // tiles of the matrices before each
+  int32_t n, tiles;
+};
+static_assert(kMx4Most <= 64, "a lane for each matrix");
 
 // Activations held so, and what their second moment goes to: one line of codes
 // and scales a feature, in blocks along the samples.
@@ -355,6 +358,7 @@ MUON_WEAK hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, con
                                                    uint32_t* flags, hipStream_t s);
 // the matrices of a list share dtype and forms; axis: 1 the form along the rows is read, 0 along the columns
 MUON_WEAK hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, RoundingSeed seed, hipStream_t s);
-MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, hipStream_t s);
+// stream: the values past the caches; every row of them begins at a multiple of 16 bytes
+MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, bool stream, hipStream_t s);
 
 }  // namespace muon
