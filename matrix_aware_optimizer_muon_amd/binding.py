@@ -7,6 +7,8 @@ or cannot be loaded, every entry point raises: there is no CPU fallback.
 
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import json
 import math
@@ -430,11 +432,21 @@ class Mx4:
 def mx4_empty(rows, cols, axis=1, device=None) -> Mx4:
     """Memory for a rows x cols matrix in 4 bits (contents undefined)."""
     torch = _torch()
+    if axis not in (0, 1):
+        raise ValueError("axis is 1 (blocks along the rows) or 0 (along the columns)")
     lines, length = (rows, cols) if axis == 1 else (cols, rows)
     blocks = -(-length // 32)
     device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-    scales = torch.empty((lines, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
-    return Mx4(torch.empty((lines, 16 * blocks), dtype=torch.uint8, device=device), scales, rows, cols, axis)
+    q = Mx4.__new__(Mx4)           # its memory is as it has to be
+    q.codes = torch.empty((lines, 16 * blocks), dtype=torch.uint8, device=device)
+    q.scales = torch.empty((lines, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
+    q.rows, q.cols, q.axis = rows, cols, axis
+    return q
+
+
+def _on(stream):
+    """Allocations inside are of that stream's memory (None: the current one's)."""
+    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _mx4_values(x):
@@ -483,11 +495,11 @@ def mx4_quantize(x, axis=1, out: Optional[Mx4] = None, rounding: str = "nearest"
     `out` if given (whose axis then counts)."""
     torch = _torch()
     mode = _rounding(rounding)
-    m, _ = _mx4_values(x)
     given = out is not None
     if not given:
-        with torch.cuda.stream(stream):       # of that stream's memory (None: the current one's)
-            out = mx4_empty(m.shape[0], m.shape[1], axis, x.device)
+        rows, cols = x.shape if x.dim() == 2 else _mx4_values(x)[0].shape
+        with _on(stream):
+            out = mx4_empty(rows, cols, axis, x.device)
     d = mx4_desc(x, out)
     _launch_on(x.device, load_library().muon_mx4_quantize, ctypes.byref(d), 1, mode, _seed64(seed),
                _raw_stream(x.device, stream))
@@ -503,7 +515,7 @@ def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     torch = _torch()
     given = out is not None
     if not given:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             out = torch.empty((q.rows, q.cols), dtype=dtype or torch.float32, device=q.device)
     elif dtype is not None and dtype != out.dtype:
         raise ValueError("out is not of the dtype asked for")
@@ -549,9 +561,13 @@ class Mx4Copies:
         self.elements = sum(r * c for r, c in shapes)
         self._shapes = shapes
         self._descs, self._n = _array([mx4_desc(t, *c) for t, c in zip(self.tensors, self.copies)], MuonMx4)
-        self._values, _ = _array(self._descs[:self._n], MuonMx4)        # with the values elsewhere: dequantize
-        for d in self._values[:self._n]:
+        # the same for values one matrix's after another's: dequantize's, with offsets of elements for addresses
+        self._elsewhere, _ = _array(self._descs[:self._n], MuonMx4)
+        self._starts, at = [], 0
+        for d in self._elsewhere[:self._n]:
             d.ld = d.cols
+            self._starts.append(at)
+            at += d.rows * d.cols
 
     def quantize(self, rounding: str = "nearest", seed: int = 0, stream=None):
         """Renew every copy from its tensor."""
@@ -569,7 +585,7 @@ class Mx4Copies:
             raise ValueError("no copies along that axis")
         given = out is not None
         if not given:
-            with torch.cuda.stream(stream):
+            with _on(stream):
                 out = torch.empty(self.elements, dtype=dtype or torch.float32, device=self.device)
         elif dtype is not None and dtype != out.dtype:
             raise ValueError("out is not of the dtype asked for")
@@ -579,10 +595,11 @@ class Mx4Copies:
         if dt is None:
             raise ValueError(f"unsupported dtype {out.dtype}")
         at, es = out.data_ptr(), out.element_size()
-        for d in self._values[:self._n]:
-            d.values, d.dtype = at, dt
-            at += d.rows * d.cols * es
-        _launch_on(self.device, load_library().muon_mx4_dequantize, self._values, self._n, axis,
+        descs = type(self._elsewhere).from_buffer_copy(self._elsewhere)
+        words, of = memoryview(descs).cast("B").cast("q"), ctypes.sizeof(MuonMx4) // 8
+        words[MuonMx4.values.offset // 8::of] = memoryview(array.array("q", [at + start * es for start in self._starts]))
+        words[MuonMx4.dtype.offset // 8::of] = memoryview(array.array("q", [dt] * self._n))      # reserved stays 0
+        _launch_on(self.device, load_library().muon_mx4_dequantize, descs, self._n, axis,
                    _raw_stream(self.device, stream))
         if stream is not None:
             out.record_stream(stream if given else torch.cuda.current_stream(self.device))

@@ -39,12 +39,6 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t 
                : "memory", "m0");
 }
 
-// The same, four bytes a lane.
-__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds)
-               : "memory", "m0");
-}
-
 // LDS byte address of a shared-memory pointer.
 template <typename E>
 __device__ __forceinline__ uint32_t lds_addr(const E* p) {

@@ -853,18 +853,21 @@ struct Mx4Launch {
 // A span of memory that a call on a list touches.
 struct Mx4Span { uintptr_t lo, hi; bool written; int32_t matrix; const char* what; };
 
+muon_status_t fail_mx4(muon_status_t st, int32_t matrix, const char* what, const char* problem) {
+  return fail(st, "matrix " + std::to_string(matrix) + ": " + what + problem);
+}
+
 // One form's lines: their addresses, alignment and span.
-muon_status_t check_mx4_form(const std::string& who, const char* what, const uint8_t* codes, const uint8_t* scales,
-                             int64_t ld_codes, int64_t ld_scales, int64_t lines, int64_t length, bool written,
-                             int32_t matrix, std::vector<Mx4Span>& spans) {
-  if (!codes || !scales) return fail(MUON_ERR_NULL_ARG, who + what + ": codes and scales go together");
+muon_status_t check_mx4_form(int32_t matrix, const char* what, const uint8_t* codes, const uint8_t* scales, int64_t ld_codes,
+                             int64_t ld_scales, int64_t lines, int64_t length, bool written, std::vector<Mx4Span>& spans) {
+  if (!codes || !scales) return fail_mx4(MUON_ERR_NULL_ARG, matrix, what, ": codes and scales go together");
   const int64_t blocks = (length + kMx4Block - 1) / kMx4Block;
   if (ld_codes < blocks * 16 || ld_scales < blocks)
-    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions below a line's blocks");
+    return fail_mx4(MUON_ERR_BAD_SHAPE, matrix, what, ": leading dimensions below a line's blocks");
   if (ld_codes > int64_t(16) << 31 || ld_scales > int64_t(4) << 31)
-    return fail(MUON_ERR_BAD_SHAPE, who + what + ": leading dimensions too large");
+    return fail_mx4(MUON_ERR_BAD_SHAPE, matrix, what, ": leading dimensions too large");
   if (reinterpret_cast<uintptr_t>(codes) % 16 || ld_codes % 16 || reinterpret_cast<uintptr_t>(scales) % 4 || ld_scales % 4)
-    return fail(MUON_ERR_ALIGNMENT, who + what + ": codes and their leading dimension are multiples of 16, scales of 4");
+    return fail_mx4(MUON_ERR_ALIGNMENT, matrix, what, ": codes and their leading dimension are multiples of 16, scales of 4");
   const uintptr_t c = reinterpret_cast<uintptr_t>(codes), e = reinterpret_cast<uintptr_t>(scales);
   spans.push_back({c, c + uintptr_t((lines - 1) * ld_codes + blocks * 16), written, matrix, "codes"});
   spans.push_back({e, e + uintptr_t((lines - 1) * ld_scales + blocks), written, matrix, "scales"});
@@ -895,25 +898,26 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
   spans.reserve(size_t(n) * 5);
   for (int32_t i = 0; i < n; ++i) {
     const muon_mx4_t& x = list[i];
-    const std::string who = "matrix " + std::to_string(i) + ": ";
-    if (!x.values) return fail(MUON_ERR_NULL_ARG, who + "values is NULL");
-    if (x.dtype != MUON_F32 && x.dtype != MUON_BF16) return fail(MUON_ERR_BAD_DTYPE, who + "dtype must be MUON_F32 or MUON_BF16");
+    if (!x.values) return fail_mx4(MUON_ERR_NULL_ARG, i, "", "values is NULL");
+    if (x.dtype != MUON_F32 && x.dtype != MUON_BF16)
+      return fail_mx4(MUON_ERR_BAD_DTYPE, i, "", "dtype must be MUON_F32 or MUON_BF16");
     constexpr int64_t most = int64_t(1) << 30;
     if (x.rows < 1 || x.cols < 1 || x.rows > most || x.cols > most)
-      return fail(MUON_ERR_BAD_SHAPE, who + "rows and cols must be in [1, 2^30]");
-    if (x.ld < x.cols) return fail(MUON_ERR_BAD_SHAPE, who + "the leading dimension must be >= cols");
-    if (x.reserved != 0) return fail(MUON_ERR_BAD_ARG, who + "reserved must be 0");
+      return fail_mx4(MUON_ERR_BAD_SHAPE, i, "", "rows and cols must be in [1, 2^30]");
+    if (x.ld < x.cols) return fail_mx4(MUON_ERR_BAD_SHAPE, i, "", "the leading dimension must be >= cols");
+    if (x.reserved != 0) return fail_mx4(MUON_ERR_BAD_ARG, i, "", "reserved must be 0");
     const size_t es = x.dtype == MUON_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail(MUON_ERR_ALIGNMENT, who + "values misaligned");
+    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail_mx4(MUON_ERR_ALIGNMENT, i, "", "values misaligned");
     const bool row = axis != 0 && (x.row_codes || x.row_scales || axis == 1);
     const bool col = axis != 1 && (x.col_codes || x.col_scales || axis == 0);
-    if (!row && !col) return fail(MUON_ERR_NULL_ARG, who + "no form is given");
+    if (!row && !col) return fail_mx4(MUON_ERR_NULL_ARG, i, "", "no form is given");
     muon_status_t st = MUON_OK;
-    if (row) st = check_mx4_form(who, "form along the rows", x.row_codes, x.row_scales, x.ld_row_codes, x.ld_row_scales,
-                                 x.rows, x.cols, quantize, i, spans);
+    if (row)
+      st = check_mx4_form(i, "form along the rows", x.row_codes, x.row_scales, x.ld_row_codes, x.ld_row_scales, x.rows,
+                          x.cols, quantize, spans);
     if (st == MUON_OK && col)
-      st = check_mx4_form(who, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales,
-                          x.cols, x.rows, quantize, i, spans);
+      st = check_mx4_form(i, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales, x.cols,
+                          x.rows, quantize, spans);
     if (st != MUON_OK) return st;
     const uintptr_t v = reinterpret_cast<uintptr_t>(x.values);
     spans.push_back({v, v + uintptr_t((x.rows - 1) * x.ld + x.cols) * es, !quantize, i, "values"});
@@ -938,7 +942,7 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
       d.col_ld4 = uint32_t(x.ld_col_scales / 4);
     }
     const int64_t tiles = (x.rows + kMx4Tile - 1) / kMx4Tile * d.tiles_c;
-    if (tiles > kMx4MaxTiles) return fail(MUON_ERR_UNSUPPORTED, who + "more than 2^24 - 1 tiles of 128 x 128");
+    if (tiles > kMx4MaxTiles) return fail_mx4(MUON_ERR_UNSUPPORTED, i, "", "more than 2^24 - 1 tiles of 128 x 128");
     Mx4Launch* to = nullptr;    // the latest launch of this kind, if it has room
     for (Mx4Launch& k : out)
       if (k.f32 == f32 && k.row == row && k.col == col && k.stream == streams) to = &k;
