@@ -241,8 +241,8 @@ muon_status_t muon_precond_refresh_accumulated(muon_handle_t h, int32_t slot, in
  * bytes (at most 2^24 each) from the next.  Otherwise as
  * muon_precond_refresh and muon_precond_accumulate, but for beta in float64:
  * Sigma and N are decayed by the same factor, in float64, Sigma then rounded.
- * The products are exact in float32 and summed in it.  What lies behind the n_rows-th sample of a line is
- * not counted. */
+ * The products are exact in float32, within its range, and summed in it.  What
+ * lies behind the n_rows-th sample of a line is not counted. */
 muon_status_t muon_precond_refresh_mx4(muon_handle_t h, int32_t slot, int32_t block, const uint8_t* codes,
                                        const uint8_t* scales, int64_t n_rows, int64_t ld_codes, int64_t ld_scales,
                                        float damping, void* stream);
@@ -386,8 +386,10 @@ typedef struct {
 /* Rounds each matrix of the list to the forms it names (at least one), both from
  * one read; one launch for up to 64 matrices of one dtype and one choice of
  * forms.  Needs no handle; works on the calling thread's current device,
- * asynchronous on `stream`.  The forms' spans must not overlap each other or any
- * values of the list.  `seed` is of use only for MUON_ROUND_RANDOM. */
+ * asynchronous on `stream`.  The forms' spans (from the first byte to the last,
+ * what lies between lines included) must not overlap each other or any values of
+ * the list.  `seed` is of use only for MUON_ROUND_RANDOM; a captured call keeps
+ * its seed in every replay. */
 muon_status_t muon_mx4_quantize(const muon_mx4_t* list, int32_t n, int32_t rounding, uint64_t seed, void* stream);
 
 /* Writes the values that each matrix's form along its rows (axis 1) or columns

@@ -857,6 +857,18 @@ muon_status_t fail_mx4(muon_status_t st, int32_t matrix, const char* what, const
   return fail(st, "matrix " + std::to_string(matrix) + ": " + what + problem);
 }
 
+// Adds the span of `lines` lines, `ld` bytes apart and `last` bytes of the last one; false past the end of all addresses.
+bool mx4_span(const void* at, int64_t lines, int64_t ld, int64_t last, bool written, int32_t matrix, const char* what,
+              std::vector<Mx4Span>& spans) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(at);
+  uintptr_t hi;
+  if (__builtin_mul_overflow(uintptr_t(lines - 1), uintptr_t(ld), &hi) || __builtin_add_overflow(hi, uintptr_t(last), &hi) ||
+      __builtin_add_overflow(hi, lo, &hi))
+    return false;
+  spans.push_back({lo, hi, written, matrix, what});
+  return true;
+}
+
 // One form's lines: their addresses, alignment and span.
 muon_status_t check_mx4_form(int32_t matrix, const char* what, const uint8_t* codes, const uint8_t* scales, int64_t ld_codes,
                              int64_t ld_scales, int64_t lines, int64_t length, bool written, std::vector<Mx4Span>& spans) {
@@ -868,9 +880,9 @@ muon_status_t check_mx4_form(int32_t matrix, const char* what, const uint8_t* co
     return fail_mx4(MUON_ERR_BAD_SHAPE, matrix, what, ": leading dimensions too large");
   if (reinterpret_cast<uintptr_t>(codes) % 16 || ld_codes % 16 || reinterpret_cast<uintptr_t>(scales) % 4 || ld_scales % 4)
     return fail_mx4(MUON_ERR_ALIGNMENT, matrix, what, ": codes and their leading dimension are multiples of 16, scales of 4");
-  const uintptr_t c = reinterpret_cast<uintptr_t>(codes), e = reinterpret_cast<uintptr_t>(scales);
-  spans.push_back({c, c + uintptr_t((lines - 1) * ld_codes + blocks * 16), written, matrix, "codes"});
-  spans.push_back({e, e + uintptr_t((lines - 1) * ld_scales + blocks), written, matrix, "scales"});
+  if (!mx4_span(codes, lines, ld_codes, blocks * 16, written, matrix, "codes", spans) ||
+      !mx4_span(scales, lines, ld_scales, blocks, written, matrix, "scales", spans))
+    return fail_mx4(MUON_ERR_BAD_SHAPE, matrix, what, ": leading dimensions too large");
   return MUON_OK;
 }
 
@@ -906,8 +918,8 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
       return fail_mx4(MUON_ERR_BAD_SHAPE, i, "", "rows and cols must be in [1, 2^30]");
     if (x.ld < x.cols) return fail_mx4(MUON_ERR_BAD_SHAPE, i, "", "the leading dimension must be >= cols");
     if (x.reserved != 0) return fail_mx4(MUON_ERR_BAD_ARG, i, "", "reserved must be 0");
-    const size_t es = x.dtype == MUON_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(x.values) % es) return fail_mx4(MUON_ERR_ALIGNMENT, i, "", "values misaligned");
+    const int64_t es = x.dtype == MUON_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x.values) % uintptr_t(es)) return fail_mx4(MUON_ERR_ALIGNMENT, i, "", "values misaligned");
     const bool row = axis != 0 && (x.row_codes || x.row_scales || axis == 1);
     const bool col = axis != 1 && (x.col_codes || x.col_scales || axis == 0);
     if (!row && !col) return fail_mx4(MUON_ERR_NULL_ARG, i, "", "no form is given");
@@ -919,8 +931,9 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
       st = check_mx4_form(i, "form along the columns", x.col_codes, x.col_scales, x.ld_col_codes, x.ld_col_scales, x.cols,
                           x.rows, quantize, spans);
     if (st != MUON_OK) return st;
-    const uintptr_t v = reinterpret_cast<uintptr_t>(x.values);
-    spans.push_back({v, v + uintptr_t((x.rows - 1) * x.ld + x.cols) * es, !quantize, i, "values"});
+    if (x.ld > INT64_MAX / es ||
+        !mx4_span(x.values, x.rows, x.ld * es, x.cols * es, !quantize, i, "values", spans))
+      return fail_mx4(MUON_ERR_BAD_SHAPE, i, "", "the leading dimension is too large");
     const bool f32 = x.dtype == MUON_F32;
     Mx4Dev d;
     std::memset(&d, 0, sizeof(d));

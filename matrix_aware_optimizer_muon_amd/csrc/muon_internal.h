@@ -317,12 +317,12 @@ hipError_t launch_precond_accumulate(const PrecondBlockDev& b, const void* acts,
                                      bool acts_f32, float beta, hipStream_t s);
 hipError_t launch_precond_refresh_accumulated(const PrecondBlockDev& b, float damping, bool reset, uint32_t* flags,
                                               hipStream_t s);
-// tasks: n_bf16 tiles of bf16-gradient tensors, then n_f32 of float32 ones
 // floats that the scratch of a block's partial sums holds at the least
 inline size_t moment_part_floats(int dp) {
   const size_t sq = size_t(dp) * dp, splits = size_t(moment_splits(dp, false, INT64_MAX));
   return sq * (splits > 2 ? splits : 2);
 }
+// tasks: n_bf16 tiles of bf16-gradient tensors, then n_f32 of float32 ones
 hipError_t launch_precond_apply(const PrecondDev* pds, const ApplyTask* tasks, int n_bf16, int n_f32, hipStream_t s);
 hipError_t launch_identity(uint16_t* sinv, int dp, int nblocks, hipStream_t s);
 hipError_t launch_adam_tick(AdamState* st, float beta1, float beta2, hipStream_t s);

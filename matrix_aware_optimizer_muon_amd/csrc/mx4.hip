@@ -10,9 +10,9 @@
 // gfx950 converts two float32 or bf16 to e2m1 with their scale in one
 // instruction (nearest, ties to even, saturating), and one at random:
 // floor(a / step + seed / 2^32) in the code's binade, of which the seed's upper
-// 22 bits count for float32 (fewer for bf16, which is widened first therefore).  Its scale operand is a float32 of which the exponent field
-// alone is read, so e << 23 serves for every e, 0 (2^-127) and 255 (NaN)
-// included.
+// 22 bits count for float32 (fewer for bf16, which is widened first therefore).
+// Its scale operand is a float32 of which the exponent field alone is read, so
+// e << 23 serves for every e, 0 (2^-127) and 255 (NaN) included.
 //
 // Bound by memory: 2 or 4 bytes read and 17/32 written an element and form.
 #include <type_traits>

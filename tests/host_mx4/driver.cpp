@@ -79,6 +79,19 @@ static void check_launches() {
     CHECK(l.tiles == tiles, "%d tiles of %ld", l.tiles, long(tiles));
   }
   for (int k = 0; k < 300; ++k) CHECK(seen[k] == 1, "matrix %d in %d launches", k, seen[k]);
+  // leading dimensions whose span passes the end of all addresses
+  const auto refused = [](int64_t rows, int64_t ld, int64_t ld_codes, int64_t ld_scales, const char* why) {
+    muon_mx4_t x = matrix(0, rows, 32, MUON_F32, true, false);
+    x.ld = ld, x.ld_row_codes = ld_codes, x.ld_row_scales = ld_scales;
+    for (auto call : {+[](const muon_mx4_t* m) { return muon_mx4_quantize(m, 1, 0, 0, nullptr); },
+                      +[](const muon_mx4_t* m) { return muon_mx4_dequantize(m, 1, 1, nullptr); }})
+      CHECK(call(&x) == MUON_ERR_BAD_SHAPE && std::string(muon_last_error()).find(why) != std::string::npos, "%s: %s", why,
+            muon_last_error());
+  };
+  refused(1 << 30, 32, int64_t(1) << 35, 4, "along the rows: leading dimensions too large");
+  refused(1 << 30, INT64_MAX, 16, 4, "the leading dimension is too large");
+  refused(1 << 30, INT64_MAX / 4, 16, 4, "the leading dimension is too large");
+  refused(2, INT64_MAX, 16, 4, "the leading dimension is too large");
   // Reading back: streamed where the rows allow it; a small list of both kinds is one launch, a large one two.
   const auto back = [&](std::vector<muon_mx4_t> l, int axis) {
     g_lists.clear(), g_what.clear();
