@@ -456,6 +456,8 @@ def _mx4_values(x):
     dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(x.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
+    if not x.numel():
+        raise ValueError("an empty tensor has no 4-bit form")
     x = _adam_matrix(x)
     if x.shape[1] > 1 and x.stride(1) != 1:
         raise ValueError("tensors must be row-major (unit column stride)")

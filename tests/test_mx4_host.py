@@ -8,6 +8,7 @@ import pytest
 
 import matrix_aware_optimizer_muon_amd as mm
 from matrix_aware_optimizer_muon_amd import binding as B
+from tests.test_binding_device_host import World
 
 torch = pytest.importorskip("torch")
 lib = B.load_library()
@@ -134,6 +135,11 @@ def test_binding_refusals():
         with pytest.raises(ValueError):
             mm.Mx4(codes, scales, rows, cols, axis)
     form = mm.Mx4(u8(4, 32), u8(4, 4), 4, 33)
+    for shape in ((), (0,), (0, 4), (4, 0), (0, 3, 4)):
+        with pytest.raises(ValueError):
+            mm.mx4_quantize(torch.zeros(shape))
+        with pytest.raises(ValueError):
+            mm.Mx4Copies([torch.zeros(shape)])
     with pytest.raises(ValueError):
         mm.mx4_desc(torch.zeros(5, 33), form)
     with pytest.raises(ValueError):
@@ -179,3 +185,12 @@ def test_descriptions():
 def test_exported_and_declared():
     assert {"muon_mx4_quantize", "muon_mx4_dequantize"} <= set(mm.header_functions())
     assert ctypes.sizeof(mm.MuonMx4) == 104
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_calls_run_on_the_tensors_device(monkeypatch, index):
+    """As a handle's do: the library is called with the tensors' device the current one, and its stream."""
+    world = World()
+    monkeypatch.setattr(B, "_torch", lambda: world)
+    B._launch_on(torch.device("cuda", index), world.muon_mx4_quantize, None, 0, 0, 0, None)
+    assert world.calls == [("muon_mx4_quantize", index)] and world.current == 0
