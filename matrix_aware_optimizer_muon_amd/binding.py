@@ -8,7 +8,6 @@ or cannot be loaded, every entry point raises: there is no CPU fallback.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
 import json
 import math
@@ -369,8 +368,8 @@ def _raw_stream(device, stream):
         raise ValueError("the tensors must be on a GPU")
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if stream is None and raw is not None:
-        return ctypes.c_void_p(raw(device.index))
-    return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+        return raw(device.index)
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
 
 
 def _launch_on(device, function, *args):
@@ -390,7 +389,7 @@ class Mx4:
     >= 16 * blocks] and `scales` uint8 [lines, >= blocks], on one device, each
     with unit stride in a line; lines begin at multiples of 16 and 4 bytes."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "axis")
+    __slots__ = ("codes", "scales", "rows", "cols", "axis", "_leading")
 
     def __init__(self, codes, scales, rows, cols, axis=1):
         if axis not in (0, 1):
@@ -405,24 +404,21 @@ class Mx4:
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
         self.codes, self.scales, self.rows, self.cols, self.axis = codes, scales, rows, cols, axis
+        # bytes between lines of codes and of scales (a single line's own width: its stride says nothing)
+        self._leading = [t.stride(0) if lines > 1 else -(-t.shape[1] // unit) * unit
+                         for t, unit in ((codes, 16), (scales, 4))]
 
     @property
     def device(self):
         return self.codes.device
 
-    def _leading(self):
-        """Bytes between lines of codes and of scales (a single line's own width: its stride says nothing)."""
-        return [t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
-                for t, unit in ((self.codes, 16), (self.scales, 4))]
-
     def _describe(self, d):
-        ld_codes, ld_scales = self._leading()
         if self.axis == 1:
             d.row_codes, d.row_scales = self.codes.data_ptr(), self.scales.data_ptr()
-            d.ld_row_codes, d.ld_row_scales = ld_codes, ld_scales
+            d.ld_row_codes, d.ld_row_scales = self._leading
         else:
             d.col_codes, d.col_scales = self.codes.data_ptr(), self.scales.data_ptr()
-            d.ld_col_codes, d.ld_col_scales = ld_codes, ld_scales
+            d.ld_col_codes, d.ld_col_scales = self._leading
 
     def record_stream(self, stream):
         self.codes.record_stream(stream)
@@ -438,42 +434,45 @@ def mx4_empty(rows, cols, axis=1, device=None) -> Mx4:
     blocks = -(-length // 32)
     device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     q = Mx4.__new__(Mx4)           # its memory is as it has to be
-    q.codes = torch.empty((lines, 16 * blocks), dtype=torch.uint8, device=device)
-    q.scales = torch.empty((lines, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
-    q.rows, q.cols, q.axis = rows, cols, axis
+    ld_codes, ld_scales = 16 * blocks, -(-blocks // 4) * 4
+    q.codes = torch.empty_strided((lines, ld_codes), (ld_codes, 1), dtype=torch.uint8, device=device)
+    q.scales = torch.empty_strided((lines, ld_scales), (ld_scales, 1), dtype=torch.uint8, device=device)
+    q.rows, q.cols, q.axis, q._leading = rows, cols, axis, (ld_codes, ld_scales)
     return q
 
 
-def _on(stream):
-    """Allocations inside are of that stream's memory (None: the current one's)."""
-    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+def _on(stream, make):
+    """What make() allocates, of that stream's memory (None: the current one's)."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
 
 
 def _mx4_values(x):
     """A tensor as the matrix that its 4-bit forms are those of (a vector as 1 x n, more dimensions as shape[0] x
     rest), and the ABI's dtype of its elements."""
     torch = _torch()
-    dt = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}.get(x.dtype)
-    if dt is None:
-        raise ValueError(f"unsupported dtype {x.dtype}")
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"unsupported dtype {dtype}")
     if not x.numel():
         raise ValueError("an empty tensor has no 4-bit form")
-    x = _adam_matrix(x)
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    if x.dim() != 2:
+        x = _adam_matrix(x)
+    if x.stride(1) != 1 and x.shape[1] > 1:
         raise ValueError("tensors must be row-major (unit column stride)")
-    return x, dt
+    return x, MUON_BF16 if dtype is torch.bfloat16 else MUON_F32
 
 
 def mx4_desc(values, *forms) -> MuonMx4:
     """The ABI's description of a matrix with its forms (at most one each way)."""
     x, dt = _mx4_values(values)
-    d = MuonMx4()
-    d.values, d.dtype = x.data_ptr(), dt
-    d.rows, d.cols = x.shape
-    d.ld = x.stride(0) if x.shape[0] > 1 else d.cols
+    rows, cols = x.shape
+    d = MuonMx4(x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols, dt)
     for f in forms:
-        if (f.rows, f.cols) != tuple(x.shape):
-            raise ValueError(f"a form of a {f.rows} x {f.cols} matrix for one of {d.rows} x {d.cols}")
+        if f.rows != rows or f.cols != cols:
+            raise ValueError(f"a form of a {f.rows} x {f.cols} matrix for one of {rows} x {cols}")
         if f.device != x.device:
             raise ValueError("values and forms must be on one device")
         f._describe(d)
@@ -487,7 +486,7 @@ def _rounding(rounding):
 
 
 def _seed64(seed):
-    return ctypes.c_uint64(int(seed) & (2 ** 64 - 1))
+    return int(seed) & 0xffffffffffffffff
 
 
 def mx4_quantize(x, axis=1, out: Optional[Mx4] = None, rounding: str = "nearest", seed: int = 0, stream=None) -> Mx4:
@@ -500,8 +499,7 @@ def mx4_quantize(x, axis=1, out: Optional[Mx4] = None, rounding: str = "nearest"
     given = out is not None
     if not given:
         rows, cols = x.shape if x.dim() == 2 else _mx4_values(x)[0].shape
-        with _on(stream):
-            out = mx4_empty(rows, cols, axis, x.device)
+        out = _on(stream, lambda: mx4_empty(rows, cols, axis, x.device))
     d = mx4_desc(x, out)
     _launch_on(x.device, load_library().muon_mx4_quantize, ctypes.byref(d), 1, mode, _seed64(seed),
                _raw_stream(x.device, stream))
@@ -517,8 +515,7 @@ def mx4_dequantize(q: Mx4, dtype=None, out=None, stream=None):
     torch = _torch()
     given = out is not None
     if not given:
-        with _on(stream):
-            out = torch.empty((q.rows, q.cols), dtype=dtype or torch.float32, device=q.device)
+        out = _on(stream, lambda: torch.empty((q.rows, q.cols), dtype=dtype or torch.float32, device=q.device))
     elif dtype is not None and dtype != out.dtype:
         raise ValueError("out is not of the dtype asked for")
     d = mx4_desc(out, q)
@@ -587,8 +584,7 @@ class Mx4Copies:
             raise ValueError("no copies along that axis")
         given = out is not None
         if not given:
-            with _on(stream):
-                out = torch.empty(self.elements, dtype=dtype or torch.float32, device=self.device)
+            out = _on(stream, lambda: torch.empty(self.elements, dtype=dtype or torch.float32, device=self.device))
         elif dtype is not None and dtype != out.dtype:
             raise ValueError("out is not of the dtype asked for")
         elif out.shape != (self.elements,) or not out.is_contiguous() or out.device != self.device:
@@ -734,7 +730,7 @@ class MuonStep:
                 raise ValueError(f"activations of {acts.cols} features for a slot of {self._pcs[slot].d}")
             if acts.device != self.device:
                 raise ValueError(f"activations on {acts.device} for a handle on {self.device}")
-            ld_codes, ld_scales = acts._leading()
+            ld_codes, ld_scales = acts._leading
             self._launch(getattr(self._lib, f"muon_precond_{name}_mx4"), self._h, slot, block, acts.codes.data_ptr(),
                          acts.scales.data_ptr(), acts.rows, ld_codes, ld_scales, scalar,
                          ctypes.c_void_p(s.cuda_stream))

@@ -156,6 +156,13 @@ __device__ __forceinline__ uint32_t group_hash(uint32_t key, uint32_t row, uint3
 // not meet in a bank.
 __device__ __forceinline__ int turned(int r, int c) { return r * kTile + ((c + (r & ~31)) & (kTile - 1)); }
 
+// The hash of row r's 16 columns g of a tile: a column's rows follow each other,
+// and the four bands, and the eight groups, begin in different banks: a quarter
+// of the LDS reads that they take row by row, and none of the conflicts (4099 x
+// 1025 bf16 at random along the columns 7.1 -> 6.9 us).
+constexpr int kHashPitch = kTile + 12;
+__device__ __forceinline__ int hash_at(int r, int g) { return g * kHashPitch + r + (r >> 5) * 4; }
+
 // Four threads have the elements of a block.
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, true)));   // lanes 1 0 3 2
@@ -235,7 +242,7 @@ template <bool F32, bool ROW, bool COL, bool RANDOM, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const Mx4List l, const RoundingSeed seed) {
   using E = typename std::conditional<F32, uint32_t, uint16_t>::type;
   __shared__ __attribute__((aligned(16))) E smem[COL ? kTile * kTile : 8];
-  __shared__ uint32_t hashes[COL && RANDOM ? kTile * kTile / 16 : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t hashes[COL && RANDOM ? kTile / 16 * kHashPitch : 1];
   const Tile t = find_tile(l);
   const Mx4Dev& m = t.m;
   const int q = threadIdx.x % kChunks, rq = threadIdx.x / kChunks;
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const Mx4List l, con
       for (int k = 0; k < Chunk<F32>::N; ++k)
         *reinterpret_cast<u32x4_t*>(smem + turned(lr, q * 8) + 4 * k) = real ? u32x4_t(x[p].w[k]) : u32x4_t{0u, 0u, 0u, 0u};
       if constexpr (RANDOM)
-        if ((q & 1) == 0) hashes[lr * (kTile / 16) + (q >> 1)] = hash;
+        if ((q & 1) == 0) hashes[hash_at(lr, q >> 1)] = hash;
     }
   }
   if constexpr (COL) {
@@ -326,9 +333,13 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const Mx4List l, con
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t words[8];
+        u32x4_t hash[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          words[k] = RANDOM ? hashes[(band * 32 + g * 8 + k) * (kTile / 16) + (lc >> 4)] + ((lc & 15) + s) * kGolden : 0u;
+        for (int k = 0; k < 2; ++k)
+          hash[k] = RANDOM ? *reinterpret_cast<const u32x4_t*>(hashes + (RANDOM ? hash_at(band * 32 + g * 8 + k * 4, lc >> 4) : 0))
+                           : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) words[k] = RANDOM ? hash[k >> 2][k & 3] + ((lc & 15) + s) * kGolden : 0u;
         w[g] = codes8<RANDOM, F32>(v[s] + g * 4, e, words);
       }
       gst(m.col.codes + (static_cast<size_t>(cc + s) * m.col_ld16 + (r >> 5)) * 16, w);
