@@ -374,7 +374,8 @@ __device__ __forceinline__ u32x4_t decode(uint32_t w, uint32_t e) {
 }
 
 // STREAM: past the caches, as the values are not read again here (246 M bf16
-// elements 87 us, 148 not).  Not for rows that do not begin at multiples of 16
+// elements 87 us, 148 not, over and over into the same buffer; into one after
+// another 115).  Not for rows that do not begin at multiples of 16
 // bytes (65536 x 1601 bf16: 81 us streamed, 40 not).
 template <bool F32, bool STREAM>
 __device__ __forceinline__ void store_values(const Mx4Dev& m, int r, int c, const u32x4_t& w) {
