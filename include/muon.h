@@ -367,7 +367,9 @@ muon_status_t muon_unpack_moments(muon_handle_t h, void* values, int32_t dtype, 
  *             2), r the upper 22 bits of a word that is a function of (seed,
  *             place in the list, row, column), the same for both forms
  * A block with an element that is not finite has e = 255 and zero codes, and
- * reads back as NaN throughout.  Reading back is exact, in float32 and bf16. */
+ * reads back as NaN throughout.  Reading back is exact, in float32 and bf16; of
+ * scales above 252, which others may have written, 4 and 6 (253) and 2 to 6
+ * (254) are beyond either and read back as infinite. */
 typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_RANDOM = 1 } muon_rounding_t;
 
 typedef struct {

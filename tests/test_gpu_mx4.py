@@ -205,3 +205,16 @@ def test_more_than_4_gib_of_codes():
     want = mm.mx4_dequantize(few, dtype=torch.bfloat16)[:1]
     for at in range(0, rows, 11000):
         assert torch.equal(back[at:at + 11000], want.expand(11000, cols))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("axis", [1, 0])
+def test_every_code_and_scale_reads_back(dtype, axis):
+    """Also those that rounding never writes: scales above 252, whose larger values are beyond float32 and bfloat16."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(16).view(1, -1).repeat(256, 1).cuda()      # 256 blocks a line
+    scales = torch.arange(256, dtype=torch.uint8).view(1, -1).repeat(256, 1).cuda()
+    q = mm.Mx4(codes, scales, *((256, 8192) if axis == 1 else (8192, 256)), axis=axis)
+    out = mm.mx4_dequantize(q, dtype=DTYPES[dtype])
+    with np.errstate(over="ignore"):
+        want = orc.dequantize(codes.cpu().numpy(), scales.cpu().numpy(), q.rows, q.cols, axis).astype(np.float32)
+    assert np.array_equal(out.float().cpu().numpy(), want, equal_nan=True)
