@@ -967,6 +967,7 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
       to->col = col;
       to->stream = streams;
       to->list.n = to->list.tiles = 0;
+      std::fill_n(to->list.tile0, kMx4Most, INT32_MAX);
     }
     to->list.tile0[to->list.n] = to->list.tiles;
     to->list.m[to->list.n++] = d;

@@ -247,10 +247,10 @@ struct Mx4Dev {
 };
 struct Mx4List {
   Mx4Dev m[kMx4Most];
-  int32_t tile0[kMx4Most];             // tiles of the matrices before each
+  int32_t tile0[kMx4Most];             // tiles of the matrices before each; INT32_MAX behind the last
   int32_t n, tiles;
 };
-static_assert(kMx4Most <= 64, "a lane for each matrix");
+static_assert(kMx4Most == 64, "a lane for each matrix");
 
 // Activations held so, and what their second moment goes to: one line of codes
 // and scales a feature, in blocks along the samples.

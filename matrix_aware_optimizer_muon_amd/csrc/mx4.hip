@@ -44,8 +44,8 @@ struct Tile { Mx4Dev m; int r0, c0; };
 __device__ __forceinline__ Tile find_tile(const Mx4List& l) {
   const int die = static_cast<int>(blockIdx.x) % 8;
   const int b = die * (l.tiles / 8) + min(die, l.tiles % 8) + static_cast<int>(blockIdx.x) / 8;
-  const int lane = threadIdx.x & 63;             // each lane asks of one matrix whether it starts behind the tile
-  const uint64_t before = __ballot(lane < l.n && l.tile0[lane < l.n ? lane : 0] <= b);
+  // each lane asks of one matrix whether it starts behind the tile
+  const uint64_t before = __ballot(l.tile0[threadIdx.x & 63] <= b);
   const int k = sreg_i32(__popcll(before) - 1);
   Tile t;
   t.m = l.m[k];

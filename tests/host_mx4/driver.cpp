@@ -77,6 +77,7 @@ static void check_launches() {
       CHECK(x.dtype == first.dtype && !x.row_codes == !first.row_codes && !x.col_codes == !first.col_codes, "kinds mixed");
     }
     CHECK(l.tiles == tiles, "%d tiles of %ld", l.tiles, long(tiles));
+    for (int i = l.n; i < muon::kMx4Most; ++i) CHECK(l.tile0[i] == INT32_MAX, "behind the last");
   }
   for (int k = 0; k < 300; ++k) CHECK(seen[k] == 1, "matrix %d in %d launches", k, seen[k]);
   // leading dimensions whose span passes the end of all addresses
