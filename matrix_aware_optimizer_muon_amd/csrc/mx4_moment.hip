@@ -13,22 +13,26 @@
 // group g (lane / 32) take neighbouring blocks one after another: their scales
 // are then bytes of one word, of which each matrix instruction names one.
 //
-// Three ways, by size (launch_mx4_moment):
+// Four ways, by size (launch_mx4_moment):
 //   bands   few samples: a wave takes 32 x 32 of the output and loads its
 //           operands from memory; as many waves as there are bands.  Bound by
 //           its launch and two trips to memory: 64 samples of 768 features 4.9
 //           us, where the sums' 4.7 MB take 1
+//   64      tiles of 64 x 64, 4 waves of 32 x 32, four blocks a CU: many CUs at
+//           work on little.  Bound by a trip to memory a stage, 0.46 us: 4096
+//           samples of 1025 features 10 us (13.8 from no cache)
 //   128     tiles of 128 x 128, 4 waves of 64 x 64, two blocks a CU.  Bound by
 //           the cache lines of the operands: a CU takes in 64 GB/s alone
 //   256     tiles of 256 x 256, 8 waves of 128 x 64, one block a CU: half the
-//           operand bytes a product.  65536 samples of 6400 features 684 us,
-//           4.1 PFLOP/s of the whole tiles' products; the loop without its
+//           operand bytes a product.  65536 samples of 6400 features 667 us,
+//           4.2 PFLOP/s of the whole tiles' products; the loop without its
 //           loads takes 527, at 1.6 GHz, the clock under this load
 // Tiles that would leave CUs idle are cut into ranges of samples, whose partial
 // sums a second launch adds in order.
 // Stages of 128 samples (half a cache line a load, four stages in LDS) took 750
 // us for the same, scales loaded 4 bytes a line and stage 920 and 8 bytes 757.
 #include <algorithm>
+#include <cmath>
 
 #include "device_common.h"
 #include "lds_ring.h"
@@ -55,10 +59,12 @@ struct Cfg {
   static constexpr int CODES = 2 * BT * kStageBlocks * 16; // bytes of a stage's codes, both operands
   static constexpr int SCALES = 2 * BT * kGroup * kStageBlocks;   // of a group's scales
   static constexpr int LDS = kStages * CODES + 2 * SCALES;
-  static constexpr int BLOCKS = LDS <= 80 << 10 ? 2 : 1;   // of a CU
+  static constexpr int BLOCKS = (160 << 10) / LDS;         // of a CU: 4, 2, 1
   static constexpr int LOADS = CODES / 2 / 16 / THREADS;   // 16 bytes a lane, one operand
-  static_assert(SCALES / 2 / 16 == THREADS, "one load a lane fills a group's scales of one operand");
+  static constexpr int SCALE_WAVES = SCALES / 2 / 1024;    // whose one load fills a group's scales of one operand
+  static_assert(WAVES == SCALE_WAVES || WAVES == 2 * SCALE_WAVES, "all waves load scales, of one operand or of both");
 };
+using Cfg64 = Cfg<64, 2, 2>;
 using Cfg128 = Cfg<128, 2, 2>;
 using Cfg256 = Cfg<256, 2, 4>;
 
@@ -291,15 +297,16 @@ __global__ __launch_bounds__(C::THREADS, C::BLOCKS) void tile_kernel(const Mx4Mo
             (line + 8 <= p.d ? off : off_end) + min(chunk, chunks),
             lds0 + buf * C::CODES + o * (C::CODES / 2) + (i * C::WAVES + wave) * 1024);
     };
-    // A group's scales of one operand, 32 lines a load, two lanes a line.
+    // A group's scales of one operand (64-tiles: of both, twice), 32 lines a load, two lanes a line.
     const bool second = ((lane ^ (lane >> 4)) & 1) != 0;
     const uint32_t off_e = (lane >> 1) * static_cast<uint32_t>(p.ld_scales);
     const uint32_t off_e_end = min(lane >> 1, (p.d - 1) & 31) * static_cast<uint32_t>(p.ld_scales);
-    const auto load_scales = [&](int v, int o) {
-      const int line = (o ? fb0 : fa0) + wave * 32;
+    const auto load_scales = [&](int v, int of) {
+      const int o = C::WAVES == C::SCALE_WAVES ? of : wave / C::SCALE_WAVES, part = wave % C::SCALE_WAVES;
+      const int line = (o ? fb0 : fa0) + part * 32;
       const uint32_t half0 = half_start(kGroup * v) * kStageBlocks, half1 = half_start(kGroup * v + 2) * kStageBlocks;
       dma16(p.scales + min(line, (p.d - 1) & ~31) * p.ld_scales, (line + 32 <= p.d ? off_e : off_e_end) + (second ? half1 : half0),
-            lds0 + kStages * C::CODES + (v & 1) * C::SCALES + o * (C::SCALES / 2) + wave * 1024);
+            lds0 + kStages * C::CODES + (v & 1) * C::SCALES + o * (C::SCALES / 2) + part * 1024);
     };
     load_scales(0, 0);
     load_scales(0, 1);
@@ -460,44 +467,54 @@ __global__ __launch_bounds__(64) void band_kernel(const Mx4MomentParams p) {
 
 // How the tiles of a launch are cut: whole rounds of the chip take whole tiles,
 // and each of the `left` others is taken in as many ranges as make the time
-// least, within one more round and the room for partial sums.  A stage of
-// 128-tiles takes 0.6 us, 0.75 to 0.85 where two blocks share a CU; a second
-// launch 4 us, and a range's partial sums, written and read, 0.03 us.
-// (16384 x 768, 21 tiles: 1, 2, 4, 8, 12, 16 ranges 49, 27, 18, 17.5, 20, 22 us;
-// 4096 x 1600, 91 tiles: 1, 2, 4 ranges 19.6, 21.6, 25; 65536 x 1600: 171, 94,
-// 73 and, with 5, 70.5.)  256-tiles: 2 us a stage, four times the sums.
+// least, within one more round and the room for partial sums.
+struct Cut { int whole, splits, stages; double us; };
+
+// The time in us, fitted to measurements on activations that are in no die's
+// cache: a stage of a tile, by how crowded the CUs are (alone it waits for
+// memory, of 64-tiles a second block is nearly free); a launch that ends in whole
+// tiles, and each of them; with ranges, two launches and each range's partial
+// sums, written and read; a round before the last.  (64: 16384 x 768, 78 tiles,
+// 1, 2, 4, 8 ranges 35.5, 23.7, 17.2, 16.4; 128: 21 tiles, 1, 2, 4, 8, 12 ranges
+// 49, 29, 20, 16.7, 17.4.)
+template <int BT> struct Cost;
+template <> struct Cost<64> { static constexpr double stage = 0.46, one = 4.1, tile = 0.0067, two = 5.6, sum = 0.011, round = 0; };
+template <> struct Cost<128> { static constexpr double stage = 0.61, one = 7.8, tile = 0.016, two = 6.5, sum = 0.033, round = 8; };
+template <> struct Cost<256> { static constexpr double stage = 2.0, one = 3.5, tile = 0, two = 4.0, sum = 0.12, round = 0; };
+template <int BT>
+double crowded(int blocks) {
+  if (blocks <= kCUs) return 1.0;
+  const double each = static_cast<double>(blocks) / kCUs;
+  return BT == 64 ? std::max(1.0, 0.61 * (each + std::ceil(each)) / 2) : 1.25 + 0.2 * (each - 1.0);
+}
 template <typename C>
-int ranges(int left, int stages, int64_t fit) {
+Cut cut_tiles(const Mx4MomentParams& p, int stages) {
+  using T = Cost<C::BT>;
   constexpr int slots = kCUs * C::BLOCKS;
-  constexpr double stage = C::BT == 128 ? 0.6 : 2.0, sums = C::BT == 128 ? 0.03 : 0.12;
+  const int nt = (p.dp + C::BT - 1) / C::BT, tiles = nt * (nt + 1) / 2, left = tiles % slots, rounds = tiles / slots;
+  const double before = rounds * (stages * T::stage * crowded<C::BT>(slots) + T::round);
+  Cut best = {tiles, 0, 0, before + T::one + T::tile * tiles + (left ? stages * T::stage * crowded<C::BT>(left) : 0.0)};
+  if (!left || !p.part) return best;
+  const int64_t fit = static_cast<int64_t>(p.part_floats / (static_cast<size_t>(left) * C::SLAB));
   const int most = static_cast<int>(std::min<int64_t>(std::min(slots / left, (stages + 1) / 2), fit));
-  double least = 0;
-  int best = 1;
-  for (int k = 1; k <= most; ++k) {
-    const int nb = left * k, per = ((stages + k - 1) / k + 1) / 2 * 2;
-    const double crowded = nb > kCUs ? 1.25 + 0.2 * (nb - kCUs) / kCUs : 1.0;
-    const double us = per * stage * crowded + (k > 1 ? 4.0 + sums * nb : 3.5);
-    if (k == 1 || us < least) {
-      least = us;
-      best = k;
-    }
+  for (int k = 2; k <= most; ++k) {
+    const int per = ((stages + k - 1) / k + 1) / 2 * 2;          // pairs, but for the last range
+    const int used = (stages + per - 1) / per;                   // those that hold stages
+    const double us = before + T::two + T::tile * (tiles - left) + T::sum * left * used +
+                      per * T::stage * crowded<C::BT>(left * used);
+    if (used > 1 && us < best.us) best = {tiles - left, used, per, us};
   }
   return best;
 }
 
 template <typename C>
-hipError_t launch_tiles(Mx4MomentParams p, int stages, hipStream_t s) {
-  constexpr int slots = kCUs * C::BLOCKS;
-  const int nt = (p.dp + C::BT - 1) / C::BT, tiles = nt * (nt + 1) / 2, left = tiles % slots;
-  const int64_t fit = left && p.part ? static_cast<int64_t>(p.part_floats / (static_cast<size_t>(left) * C::SLAB)) : 1;
-  p.splits = left ? ranges<C>(left, stages, fit) : 1;
-  p.stages = ((stages + p.splits - 1) / p.splits + 1) / 2 * 2;   // pairs, but for the last range
-  p.splits = (stages + p.stages - 1) / p.stages;                 // those that hold stages
-  const int cut = p.splits > 1 ? left : 0;
-  p.whole = tiles - cut;
-  if (!cut) p.splits = 0;
-  tile_kernel<C><<<p.whole + cut * p.splits, C::THREADS, 0, s>>>(p);
-  if (cut) reduce_kernel<C><<<cut * (C::SLAB / 4 / 256), 256, 0, s>>>(p);
+hipError_t launch_tiles(Mx4MomentParams p, const Cut& cut, hipStream_t s) {
+  const int nt = (p.dp + C::BT - 1) / C::BT, others = nt * (nt + 1) / 2 - cut.whole;
+  p.whole = cut.whole;
+  p.splits = cut.splits;
+  p.stages = cut.stages;
+  tile_kernel<C><<<p.whole + others * p.splits, C::THREADS, 0, s>>>(p);
+  if (others) reduce_kernel<C><<<others * (C::SLAB / 4 / 256), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -506,11 +523,9 @@ hipError_t launch_tiles(Mx4MomentParams p, int stages, hipStream_t s) {
 hipError_t launch_mx4_moment(Mx4MomentParams p, hipStream_t s) {
   const int64_t blocks = (p.n_rows + kMx4Block - 1) / kMx4Block;
   const int stages = static_cast<int>((blocks + kStageBlocks - 1) / kStageBlocks);
-  // Bands read more of memory a product and take one launch and no barrier.
-  // Bands against 128-tiles: 768 features, 1024 samples 7.7 and 10.1 us, 2048
-  // 11.1 and 11.0; 1600 features 13.5 and 12.5, 20.3 and 14.4.  Tiles need two
-  // whole stages.
-  if (p.n_rows < 2 * kStageBlocks * kMx4Block || (stages <= 6 && p.dp <= 1024)) {
+  // Tiles need two whole stages.  With as many, 64-tiles are faster than bands: 512 samples of 768 features 5.1 and
+  // 5.5 us, 1024 5.6 and 7.2.
+  if (p.n_rows < 2 * kStageBlocks * kMx4Block) {
     const int nb = p.dp / kBand;
     band_kernel<<<nb * (nb + 1) / 2, 64, 0, s>>>(p);
     return hipGetLastError();
@@ -520,8 +535,13 @@ hipError_t launch_mx4_moment(Mx4MomentParams p, hipStream_t s) {
   // 134 and 146; 4096 features (136 tiles on 256 CUs) 350 and 320; 16384 of 2560 56 and 52.
   const int nt = (p.dp + 255) / 256, tiles = nt * (nt + 1) / 2, left = tiles % kCUs;
   const bool fills = left == 0 || left * (kCUs / left) >= kCUs * 7 / 10;
-  const bool large = p.dp >= 2048 && fills && static_cast<int64_t>(stages) * tiles >= 6000;
-  return large ? launch_tiles<Cfg256>(p, stages, s) : launch_tiles<Cfg128>(p, stages, s);
+  if (p.dp >= 2048 && fills && static_cast<int64_t>(stages) * tiles >= 6000)
+    return launch_tiles<Cfg256>(p, cut_tiles<Cfg256>(p, stages), s);
+  // 64-tiles have more CUs at work, and less to do at a tile's end; 128-tiles read half as much a product.  64 against
+  // 128 at its best, from no cache: 1024 samples of 1025 features 7.4 and 11.2 us, 4096 13.2 and 14.6, 4096 of 1600
+  // 16.5 and 19.5; 16384 of 1600 37 and 31, 4096 of 2560 27 and 23.4.
+  const Cut small = cut_tiles<Cfg64>(p, stages), large = cut_tiles<Cfg128>(p, stages);
+  return small.us < large.us ? launch_tiles<Cfg64>(p, small, s) : launch_tiles<Cfg128>(p, large, s);
 }
 
 }  // namespace muon

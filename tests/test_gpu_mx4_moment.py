@@ -87,9 +87,11 @@ def test_sums_are_exact(n, d):
 @pytest.mark.parametrize("n,d", [(511, 1300), (512, 1300), (513, 1300), (600, 1153), (767, 1281), (768, 1600), (800, 2000),
                                  (1023, 1153), (1024, 1200), (1025, 1400), (1536, 1100), (1600, 500), (1792, 130),
                                  (2303, 1290), (2816, 40), (5120, 1025), (7000, 3), (9999, 2700), (34309, 2100),
-                                 (34560, 2100), (100001, 2049)])
+                                 (34560, 2100), (100001, 2049), (4096, 2560), (5003, 2561), (8200, 2500), (9000, 3300),
+                                 (20011, 1601), (3000, 4100), (12000, 4096), (520, 5000), (2600, 5000), (700, 4200),
+                                 (65537, 700)])
 def test_sums_are_exact_in_every_way(n, d):
-    """Bands and tiles of both sizes, whole and cut, with every length of the last stage's kind.  Scales of 1: products
+    """Bands and tiles of every size, whole and cut, with every length of the last stage's kind.  Scales of 1: products
     are multiples of 1/4 up to 36, exact for 116508 samples."""
     say(f"case: sums of {n} samples, {d} features")
     opt = handle(d)

@@ -16,4 +16,4 @@ def test_debug_build_checks_every_tile(tmp_path):
     debug = _atomics("mx4_moment.hip", str(tmp_path / "debug.s"), *B.DEBUG_FLAGS)
     assert release.keys() == debug.keys()
     tiles = [n for n in debug if "tile_kernel" in n]
-    assert len(tiles) == 2 and all(debug[n] > release[n] for n in tiles)
+    assert len(tiles) == 3 and all(debug[n] > release[n] for n in tiles)
