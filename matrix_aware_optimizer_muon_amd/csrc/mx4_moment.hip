@@ -478,7 +478,7 @@ struct Cut { int whole, splits, stages; double us; };
 // 1, 2, 4, 8 ranges 35.5, 23.7, 17.2, 16.4; 128: 21 tiles, 1, 2, 4, 8, 12 ranges
 // 49, 29, 20, 16.7, 17.4.)
 template <int BT> struct Cost;
-template <> struct Cost<64> { static constexpr double stage = 0.46, one = 4.1, tile = 0.0067, two = 5.6, sum = 0.011, round = 0; };
+template <> struct Cost<64> { static constexpr double stage = 0.46, one = 4.1, tile = 0.0067, two = 6.3, sum = 0.011, round = 0; };
 template <> struct Cost<128> { static constexpr double stage = 0.61, one = 7.8, tile = 0.016, two = 6.5, sum = 0.033, round = 8; };
 template <> struct Cost<256> { static constexpr double stage = 2.0, one = 3.5, tile = 0, two = 4.0, sum = 0.12, round = 0; };
 template <int BT>
