@@ -33,9 +33,10 @@ __device__ __forceinline__ void ring_barrier() {
 // outstanding vector-memory operation in front of the next LDS read, which
 // would drain the ring.  The stage waits are therefore explicit
 // (wait_vmcnt), and the asm's memory clobber keeps LDS accesses in order
-// around it.
+// around it.  The load needs one wait state behind the write of M0, which the
+// compiler puts between its own instructions but not into an asm block.
 __device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
                : "memory", "m0");
 }
 
