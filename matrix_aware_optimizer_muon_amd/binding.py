@@ -554,8 +554,9 @@ class Mx4Copies:
         for lines, width in sizes:
             starts.append(total)
             total += -(-lines * width // 256) * 256
-        buffer = torch.empty(total, dtype=torch.uint8, device=self.device)
-        parts = iter([buffer[at:at + lines * width].view(lines, width) for at, (lines, width) in zip(starts, sizes)])
+        self._buffer = torch.empty(total, dtype=torch.uint8, device=self.device)
+        parts = iter([self._buffer[at:at + lines * width].view(lines, width)
+                      for at, (lines, width) in zip(starts, sizes)])
         self.copies = [tuple(Mx4(next(parts), next(parts), rows, cols, a) for a in self.axes) for rows, cols in shapes]
         self.elements = sum(r * c for r, c in shapes)
         self._shapes = shapes
@@ -572,6 +573,14 @@ class Mx4Copies:
         """Renew every copy from its tensor."""
         _launch_on(self.device, load_library().muon_mx4_quantize, self._descs, self._n, _rounding(rounding),
                    _seed64(seed), _raw_stream(self.device, stream))
+        if stream is not None:
+            self.record_stream(stream)
+            for t in self.tensors:
+                t.record_stream(stream)
+
+    def record_stream(self, stream):
+        """Tell torch's allocator that `stream` uses the copies' memory."""
+        self._buffer.record_stream(stream)
 
     def dequantize(self, axis: Optional[int] = None, dtype=None, out=None, stream=None):
         """The values of every copy along `axis` (default: the first one),
@@ -600,6 +609,7 @@ class Mx4Copies:
         _launch_on(self.device, load_library().muon_mx4_dequantize, descs, self._n, axis,
                    _raw_stream(self.device, stream))
         if stream is not None:
+            self.record_stream(stream)
             out.record_stream(stream if given else torch.cuda.current_stream(self.device))
         return out
 
