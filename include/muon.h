@@ -221,7 +221,8 @@ muon_status_t muon_precond_refresh(muon_handle_t h, int32_t slot, int32_t block,
  * slot `slot`,
  *     Sigma <- beta * Sigma + X^T X,    N <- beta * N + n_rows
  * (beta = 1: plain sum over micro-batches; beta < 1: older micro-batches
- * weighted down exponentially; 0 <= beta <= 1).  X^T X is formed as in
+ * weighted down exponentially; beta = 0: the sums begin anew, whatever they
+ * held; 0 <= beta <= 1).  X^T X is formed as in
  * muon_precond_refresh (bf16 or float32 MFMA, float32 sums).  Asynchronous
  * on `stream`.  The sums start at zero at muon_init(). */
 muon_status_t muon_precond_accumulate(muon_handle_t h, int32_t slot, int32_t block, const void* acts,

@@ -126,7 +126,8 @@ __device__ __forceinline__ f32x4_t quad(const f32x16_t& v, int q) {
 }
 
 __device__ __forceinline__ void count_samples(const Mx4MomentParams& p) {
-  if (p.cnt && blockIdx.x == 0 && threadIdx.x == 0) *p.cnt = p.beta * *p.cnt + static_cast<double>(p.n_rows);
+  if (p.cnt && blockIdx.x == 0 && threadIdx.x == 0)
+    *p.cnt = (p.beta != 0.0 ? p.beta * *p.cnt : 0.0) + static_cast<double>(p.n_rows);
 }
 
 // k, a constant where it is called: the byte of each scale word.

@@ -911,10 +911,11 @@ void apply_kernel(const PrecondDev* __restrict__ pds, const ApplyTask* __restric
   else apply_tile<GF32, false>(pd, t, smem);
 }
 
-// S^-1 = I for every block (the state of a slot before its first refresh).
-// Running sample count of an accumulating block: N <- beta N + n_rows.
+// Running sample count of an accumulating block: N <- beta N + n_rows; with
+// beta = 0, as of the sums, what was there does not count, finite or not.
 __global__ void count_kernel(double* cnt, float beta, int64_t n_rows) {
-  if (threadIdx.x == 0 && blockIdx.x == 0) *cnt = static_cast<double>(beta) * *cnt + static_cast<double>(n_rows);
+  if (threadIdx.x == 0 && blockIdx.x == 0)
+    *cnt = (beta != 0.f ? static_cast<double>(beta) * *cnt : 0.0) + static_cast<double>(n_rows);
 }
 
 // S = Sigma / N + damping * I (padded diagonal 1); a block with no samples
@@ -942,6 +943,7 @@ __global__ __launch_bounds__(kThreads) void clear_acc_kernel(float* __restrict__
   if (blockIdx.x == 0 && threadIdx.x == 0) *cnt = 0.0;
 }
 
+// S^-1 = I for every block (the state of a slot before its first refresh).
 __global__ __launch_bounds__(kThreads) void identity_kernel(uint16_t* __restrict__ sinv, int dp, int nblocks) {
   const size_t plane = static_cast<size_t>(dp) * dp;
   const size_t n = static_cast<size_t>(nblocks) * kSinvPlanes * plane;
