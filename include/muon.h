@@ -404,11 +404,11 @@ muon_status_t muon_mx4_dequantize(const muon_mx4_t* list, int32_t n, int32_t axi
 /* 4-bit copies of registered weights, renewed by every following muon_step as
  * its last launches, from the weights that the step has written (rounded to
  * nearest).  Each entry names a registered tensor by its values, rows, cols, ld
- * and dtype (those of the param) and the forms to fill, which lie apart from the
- * registered tensors and the workspace and stay allocated while they are set; a
- * captured step keeps the ones that it was captured with.  n = 0 switches it off.
- * Host only: the copies hold the weights from the next step on
- * (muon_mx4_quantize of the same list fills them before). */
+ * (where it has more rows than one) and dtype, those of the param, and the forms
+ * to fill, which lie apart from the registered tensors and the workspace and stay
+ * allocated while they are set; a captured step keeps the ones that it was
+ * captured with.  n = 0 switches it off.  Host only: the copies hold the weights
+ * from the next step on (muon_mx4_quantize of the same list fills them before). */
 muon_status_t muon_set_mx4_weights(muon_handle_t h, const muon_mx4_t* copies, int32_t n);
 
 /* Clipping by the global norm: with max_norm > 0 every following muon_step

@@ -1809,7 +1809,8 @@ muon_status_t muon_set_mx4_weights(muon_handle_t h, const muon_mx4_t* copies, in
     for (int32_t i = 0; i < n; ++i) {
       const muon_mx4_t& x = copies[i];
       const auto is_param = [&](const muon_tensor_t& t) {
-        return t.param == x.values && t.rows == x.rows && t.cols == x.cols && t.ld_param == x.ld && t.dtype == x.dtype;
+        return t.param == x.values && t.rows == x.rows && t.cols == x.cols && t.dtype == x.dtype &&
+               (t.rows == 1 || t.ld_param == x.ld);   // of a single row it says nothing
       };
       if (std::none_of(h->tensors.begin(), h->tensors.end(), is_param))
         return fail(MUON_ERR_BAD_ARG, "matrix " + std::to_string(i) + ": not the param of a registered tensor");
