@@ -474,9 +474,7 @@ hipError_t launch_forms(const Mx4List& l, const RoundingSeed& seed, hipStream_t 
 }
 template <bool F32>
 hipError_t launch_rounding(const Mx4List& l, bool random, const RoundingSeed& seed, hipStream_t s) {
-  // Past what the memory-side cache holds: both forms of 246 M bf16 elements 152 us streamed, 187 not; of 28 M, still
-  // in the cache, 25.4 and 23.5, one form of 105 M 48 and 39.
-  const bool stream = static_cast<int64_t>(l.tiles) * kTile * kTile * (F32 ? 4 : 2) > int64_t(256) << 20;
+  const bool stream = mx4_round_streams(l, F32);
   if (random) return stream ? launch_forms<F32, true, true>(l, seed, s) : launch_forms<F32, true, false>(l, seed, s);
   return stream ? launch_forms<F32, false, true>(l, seed, s) : launch_forms<F32, false, false>(l, seed, s);
 }
