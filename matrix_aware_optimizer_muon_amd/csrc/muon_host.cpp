@@ -897,7 +897,7 @@ muon_status_t mx4_launches(const muon_mx4_t* list, int32_t n, int axis, std::vec
   if (n < 0) return fail(MUON_ERR_BAD_ARG, "n < 0");
   if (n > 0 && !list) return fail(MUON_ERR_NULL_ARG, "list is NULL");
   const bool quantize = axis < 0;
-  // Values that are written go past the caches where their rows allow it.  A list that holds both kinds takes two
+  // Values that are written may go past the caches where their rows allow it.  A list that holds both kinds takes two
   // launches for that, which a small one is not worth.
   bool all_aligned = true;
   size_t value_bytes = 0;

@@ -261,6 +261,13 @@ inline int64_t mx4_value_bytes(const Mx4List& l, bool f32) {
   return elements * (f32 ? 4 : 2);
 }
 inline bool mx4_round_streams(const Mx4List& l, bool f32) { return mx4_value_bytes(l, f32) > int64_t(256) << 20; }
+// Whether one that reads its matrices back (their rows beginning at multiples of
+// 16 bytes) stores the values past the caches.  Up to 4 MB it gains nothing and
+// a reader waits longer (768 bf16 elements and an addition 5.2 us streamed, 4.8
+// not; 1024 x 768 float32 7.3 and 7.1).  Larger, without the reader and with it:
+// 13 MB 4.2 and 12.9 us streamed, 5.3 and 13.1 not; 34 MB 7.8 and 24.5, 9.0 and
+// 22.4; 134 MB 24 and 65, 24 and 74; 537 MB 90 and 316, 152 and 326.
+inline bool mx4_back_streams(const Mx4List& l, bool f32) { return mx4_value_bytes(l, f32) > int64_t(4) << 20; }
 
 // Activations held so, and what their second moment goes to: one line of codes
 // and scales a feature, in blocks along the samples.
@@ -368,7 +375,7 @@ MUON_WEAK hipError_t launch_precond_accumulate_mx4(const PrecondBlockDev& b, con
                                                    uint32_t* flags, hipStream_t s);
 // the matrices of a list share dtype and forms; axis: 1 the form along the rows is read, 0 along the columns
 MUON_WEAK hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, RoundingSeed seed, hipStream_t s);
-// stream: the values past the caches; every row of them begins at a multiple of 16 bytes
-MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, bool stream, hipStream_t s);
+// aligned: every row of the values begins at a multiple of 16 bytes
+MUON_WEAK hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, bool aligned, hipStream_t s);
 
 }  // namespace muon

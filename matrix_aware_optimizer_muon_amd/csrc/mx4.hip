@@ -375,8 +375,8 @@ __device__ __forceinline__ u32x4_t decode(uint32_t w, uint32_t e) {
 
 // STREAM: past the caches, as the values are not read again here (246 M bf16
 // elements 87 us, 148 not, over and over into the same buffer; into one after
-// another 115).  Not for rows that do not begin at multiples of 16
-// bytes (65536 x 1601 bf16: 81 us streamed, 40 not).
+// another 115); mx4_back_streams has the rule by size.  Not for rows that do not
+// begin at multiples of 16 bytes (65536 x 1601 bf16: 81 us streamed, 40 not).
 template <bool F32, bool STREAM>
 __device__ __forceinline__ void store_values(const Mx4Dev& m, int r, int c, const u32x4_t& w) {
   using E = typename std::conditional<F32, uint32_t, uint16_t>::type;
@@ -485,7 +485,8 @@ hipError_t launch_mx4_quantize(const Mx4List& l, bool f32, bool random, Rounding
   return f32 ? launch_rounding<true>(l, random, seed, s) : launch_rounding<false>(l, random, seed, s);
 }
 
-hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, bool stream, hipStream_t s) {
+hipError_t launch_mx4_dequantize(const Mx4List& l, bool f32, int axis, bool aligned, hipStream_t s) {
+  const bool stream = aligned && mx4_back_streams(l, f32);
   const auto of = [&](auto k) {
     constexpr bool F32 = decltype(k)::value;
     return axis ? (stream ? dequantize_kernel<F32, 1, true> : dequantize_kernel<F32, 1, false>)

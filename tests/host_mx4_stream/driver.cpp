@@ -36,6 +36,11 @@ int main() {
   CHECK(!mx4_round_streams(list({{8192, 8192}, {4096, 16384}}), false));
   CHECK(mx4_round_streams(list({{8192, 8192}, {4096, 16384}, {1, 1}}), false));
   CHECK(mx4_round_streams(list({{1, 1 << 30}}), true) && mx4_round_streams(list({{1 << 30, 1}, {1 << 30, 1}}), true));
+  // read back: from 4 MB of values on
+  using muon::mx4_back_streams;
+  CHECK(!mx4_back_streams(list({{1, 768}}), false) && !mx4_back_streams(list({{1, 1 << 20}}), true));
+  CHECK(!mx4_back_streams(list({{1024, 1024}, {1024, 1024}}), false));
+  CHECK(mx4_back_streams(list({{1024, 1024}, {1024, 1024}, {1, 1}}), false) && mx4_back_streams(list({{1025, 1024}}), true));
   if (!g_bad) std::puts("ok");
   return g_bad != 0;
 }

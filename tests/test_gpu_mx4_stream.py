@@ -75,3 +75,25 @@ def _words(seed, rows, cols):
         w = group[:, :, None] + np.arange(16, dtype=np.uint32) * orc.GOLDEN
     out[:, first * 16:] = w.reshape(rows, -1)[:, :cols - first * 16]
     return out
+
+
+@pytest.mark.parametrize("dtype", SIZES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("axis", [1, 0])
+def test_read_back_past_the_caches(dtype, axis):
+    """Values of more than 4 MB whose rows begin at multiples of 16 bytes, edges inside tiles and blocks, in a wider
+    buffer whose other bytes stay; and one of 4 MB, which is kept."""
+    for rows, cols, gap in ((2101, 1032, 8), (1301, 2052, 12), (1024, 1024, 0)):
+        es = torch.empty((), dtype=dtype).element_size()
+        if cols * es % 16 or (cols + gap) * es % 16:
+            cols, gap = cols + 4, 0
+        say(f"case: {rows}x{cols} {dtype} axis {axis}")
+        lines, blocks = (rows, -(-cols // 32)) if axis == 1 else (cols, -(-rows // 32))
+        gen = torch.Generator(device="cuda").manual_seed(rows)
+        codes = torch.randint(0, 256, (lines, 16 * blocks), generator=gen, device="cuda", dtype=torch.uint8)
+        scales = torch.randint(100, 150, (lines, -(-blocks // 4) * 4), generator=gen, device="cuda", dtype=torch.uint8)
+        scales[3, 1] = 255
+        wide = torch.full((rows, cols + gap), 5.0, dtype=dtype, device="cuda")
+        mm.mx4_dequantize(mm.Mx4(codes, scales, rows, cols, axis), out=wide[:, :cols])
+        want = orc.dequantize(codes.cpu().numpy(), scales.cpu().numpy(), rows, cols, axis)
+        assert np.array_equal(wide[:, :cols].double().cpu().numpy(), want, equal_nan=True)
+        assert bool((wide[:, cols:] == 5.0).all())
