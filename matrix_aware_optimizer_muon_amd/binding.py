@@ -629,6 +629,10 @@ class MuonStep:
     registered must stay alive and unmoved while the object is used.
     """
 
+    _mx4 = None           # the 4-bit copies that every step renews
+    _mx4_streams = ()     # the streams of the steps that have done so, as numbers
+    _mx4_captured = False
+
     def __init__(self, descs: Sequence[MuonTensor], hp: Optional[MuonHparams] = None,
                  preconds: Sequence[MuonPrecond] = (), device=None, keepalive=(), static_scratch=False,
                  library: Optional[str] = None):
@@ -717,7 +721,25 @@ class MuonStep:
         _check(status, self._lib)
 
     def step(self, lr: float = -1.0, stream=None):
-        self._launch(self._lib.muon_step, self._h, lr, self._stream(stream))
+        raw = self._stream(stream)
+        if self._mx4 is not None:
+            self._note_mx4(stream, raw.value or 0)
+        self._launch(self._lib.muon_step, self._h, lr, raw)
+
+    def _note_mx4(self, stream, raw):
+        """Before a step that renews 4-bit copies: its stream, and, where it is being captured, that the copies are
+        the graph's from now on."""
+        cuda = _torch().cuda
+        self._mx4_streams.add(raw)
+        if not self._mx4_captured:
+            if stream is None and cuda.current_device() == self.device.index:
+                captured = cuda.is_current_stream_capturing()
+            else:
+                with cuda.stream(self._torch_stream(stream)):
+                    captured = cuda.is_current_stream_capturing()
+            if captured:
+                self._mx4_captured = True
+                self._keep.append(self._mx4)
 
     def step_timed(self, lr: float = -1.0, stream=None):
         """Run one step with HIP events between launches; returns
@@ -826,12 +848,20 @@ class MuonStep:
         """Renew the 4-bit copies of registered weights at the end of every
         following step (None: no more).  The tensors of `copies` are those
         registered as params; copies.quantize() fills them before the first
-        step.  The object lives as long as the handle: a captured step goes on
-        writing to it after it is replaced."""
+        step.  The object lives until it is replaced, and as long as the
+        handle if a step was captured meanwhile, which goes on writing to it."""
         descs, n = (None, 0) if copies is None else (copies._descs, copies._n)
         self._check(self._lib.muon_set_mx4_weights(self._h, descs, n))
-        if copies is not None and not any(k is copies for k in self._keep):
-            self._keep.append(copies)
+        old = self._mx4
+        if old is copies:
+            return
+        if old is not None:
+            cuda = _torch().cuda
+            for raw in self._mx4_streams:      # steps that are not through yet
+                old.record_stream(cuda.ExternalStream(raw, device=self.device) if raw
+                                  else cuda.default_stream(self.device))
+        self._mx4, self._mx4_streams = copies, set()
+        self._mx4_captured = any(k is copies for k in self._keep)
 
     def packed_elements(self) -> int:
         """Elements of all tensors with packed moments."""
