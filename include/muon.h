@@ -255,7 +255,9 @@ muon_status_t muon_precond_accumulate_mx4(muon_handle_t h, int32_t slot, int32_t
  * float32 with leading dimension *ld, symmetric, and N, one float64 (each
  * pointer may be NULL).  Host only.  To be read and written in the order of the
  * stream that the handle is used on: for a checkpoint, or to add up the sums of
- * data-parallel ranks before a refresh. */
+ * data-parallel ranks before a refresh.  Sigma's memory has *ld rows too (d
+ * rounded up to a multiple of 128), so that it is one run of *ld * *ld floats;
+ * what lies behind d in them is zero and has to stay so. */
 muon_status_t muon_precond_sums(muon_handle_t h, int32_t slot, int32_t block, float** sums, int64_t* ld, double** count);
 
 /* One optimizer step over every registered tensor: Muon on the kind-MUON

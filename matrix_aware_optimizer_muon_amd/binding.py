@@ -788,11 +788,14 @@ class MuonStep:
         Sigma <- beta Sigma + X^T X."""
         self._acts_call("accumulate", slot, block, acts, beta, stream)
 
-    def precond_sums(self, slot: int, block: int):
+    def precond_sums(self, slot: int, block: int, padded: bool = False):
         """The running second moment of (slot, block) itself, (Sigma, N): views
-        of the workspace, d x d float32 and one float64, to read, write or
-        all-reduce in the order of the handle's stream.  Not for a static
-        handle, whose scratch is no tensor."""
+        of the workspace, d x d float32 and one float64, to read or write in
+        the order of the handle's stream.  With padded=True Sigma is the whole
+        of its memory, d rounded up to a multiple of 128 each way: contiguous,
+        as an all-reduce over data-parallel ranks needs it, with zeros behind
+        the d-th row and column that have to stay.  Not for a static handle,
+        whose scratch is no tensor."""
         if self.workspace is None:
             raise ValueError("a static handle's sums lie in no tensor")
         torch = _torch()
@@ -804,7 +807,7 @@ class MuonStep:
         def view(at, n, dtype):
             return self.workspace[at - base:at - base + n * dtype.itemsize].view(dtype)
         rows = view(sums.value, ld.value * ld.value, torch.float32).view(ld.value, ld.value)
-        return rows[:d, :d], view(count.value, 1, torch.float64)
+        return rows if padded else rows[:d, :d], view(count.value, 1, torch.float64)
 
     def precond_refresh_accumulated(self, slot: int, block: int, damping: float = 1e-4, reset: bool = True,
                                     stream=None):
