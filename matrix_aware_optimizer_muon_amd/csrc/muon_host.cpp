@@ -1776,6 +1776,7 @@ size_t muon_packed_moment_bytes(int64_t n) { return n > 0 && n <= kPackMaxElems 
 muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed) {
   return guarded([&]() -> muon_status_t {
     if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
     h->rounding_seed = seed;
     return MUON_OK;
   });
@@ -1784,6 +1785,7 @@ muon_status_t muon_set_rounding_seed(muon_handle_t h, uint64_t seed) {
 muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* norm_out) {
   return guarded([&]() -> muon_status_t {
     if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
     if (!(max_norm >= 0.f)) return fail(MUON_ERR_BAD_ARG, "max_norm must be >= 0");
     if (max_norm == 0.f) norm_out = nullptr;
     if (max_norm > 0.f && !h->plan.with_norm)
@@ -1803,6 +1805,7 @@ muon_status_t muon_set_max_grad_norm(muon_handle_t h, float max_norm, float* nor
 muon_status_t muon_set_mx4_weights(muon_handle_t h, const muon_mx4_t* copies, int32_t n) {
   return guarded([&]() -> muon_status_t {
     if (!h) return fail(MUON_ERR_NULL_ARG, "handle is NULL");
+    if (check_live(h) != MUON_OK) return MUON_ERR_BAD_ARG;
     std::vector<Mx4Launch> launches;
     muon_status_t st = mx4_launches(copies, n, -1, launches);
     if (st != MUON_OK) return st;
