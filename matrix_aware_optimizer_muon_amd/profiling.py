@@ -18,7 +18,8 @@
 
 Kernels are named by phase: gram (A = s X X^T), square (B = bA + cA^2),
 bx (X <- s(aX + BX), weight update in the last iteration), momentum, update,
-and the Newton-Muon kernels by their own names.
+and the Newton-Muon kernels by their own names; torch's are "torch", which the
+traffic summary leaves out.
 """
 
 import argparse
@@ -47,6 +48,8 @@ def kernel_source_hash():
 
 
 def kernel_kind(name):
+    if re.search(r"\bat::native::|N2at6native", name):   # tensors made and filled around the step
+        return "torch"
     # ns_gemm_kernel<f32, phase, tile shape, last iteration>
     m = re.search(r"ns_gemm_kernel<(\w+), (\d)[,>]", name) or re.search(r"ns_gemm_kernelILb(\d)ELi(\d)E", name)
     if m:
@@ -295,7 +298,7 @@ def traffic(fetch_dir, write_dir, copy_fetch_dir, copy_write_dir, copy_bytes, co
     w_scale = copy_bytes / (cw * 1024.0)
     per = {}
     for k in sorted(set(fetch) | set(write)):
-        if k in ("copy", "fill"):
+        if k in ("copy", "fill", "torch"):
             continue
         rd = fetch.get(k, 0.0) * 1024.0 * f_scale
         wr = write.get(k, 0.0) * 1024.0 * w_scale
