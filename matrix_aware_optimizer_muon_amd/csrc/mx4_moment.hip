@@ -19,18 +19,22 @@
 //           its launch and two trips to memory: 64 samples of 768 features 4.9
 //           us, where the sums' 4.7 MB take 1
 //   64      tiles of 64 x 64, 4 waves of 32 x 32, four blocks a CU: many CUs at
-//           work on little.  Bound by a trip to memory a stage, 0.46 us: 4096
-//           samples of 1025 features 10 us (13.8 from no cache)
+//           work on little.  Bound by a trip to memory a stage: 4096 samples of
+//           1025 features 10 us (14 from no cache); 5003 of them 15, 10 without
+//           the loop's loads
 //   128     tiles of 128 x 128, 4 waves of 64 x 64, two blocks a CU.  Bound by
-//           the cache lines of the operands: a CU takes in 64 GB/s alone
+//           its loads: 65536 samples of 4096 features 315 us, 280 without the
+//           products (4.7 GB of operands, 66 GB/s a CU), 206 without the loads
 //   256     tiles of 256 x 256, 8 waves of 128 x 64, one block a CU: half the
-//           operand bytes a product.  65536 samples of 6400 features 667 us,
-//           4.2 PFLOP/s of the whole tiles' products; the loop without its
-//           loads takes 527, at 1.6 GHz, the clock under this load
+//           operand bytes a product.  Bound by loads and products alike: 65536
+//           samples of 6400 features 638 us, 4.4 PFLOP/s of the whole tiles'
+//           products; 526 without the loads, at 1.6 GHz, the clock under this
+//           load, and 613 without the products
 // Tiles that would leave CUs idle are cut into ranges of samples, whose partial
 // sums a second launch adds in order.
-// Stages of 128 samples (half a cache line a load, four stages in LDS) took 750
-// us for the same, scales loaded 4 bytes a line and stage 920 and 8 bytes 757.
+// For the last of these, when it took 684 us: stages of 128 samples (half a cache
+// line a load, four stages in LDS) 750, scales loaded 4 bytes a line and stage
+// 920, 8 bytes 757.
 #include <algorithm>
 #include <cmath>
 
@@ -479,7 +483,7 @@ struct Cut { int whole, splits, stages; double us; };
 // of 512 to 65536 samples of 64 to 6400 features, each with tiles of 64 and 128
 // whole and in up to 24 ranges: on all of them the way taken is within 5.2 % of the
 // best one measured, 0.9 % on average.  From a die's cache fewer ranges of smaller
-// tiles would often be faster (8192 samples of 1025 features 18.8 us for 15.3).
+// tiles would often be faster (8192 samples of 1025 features 18.7 us for 15.0).
 template <int BT> struct Cost;
 template <> struct Cost<64> { static constexpr double stage = 0.55, one = 3.5, tile = 0.0035, two = 6.0, sum = 0.0101, round = 0; };
 template <> struct Cost<128> { static constexpr double stage = 0.81, one = 6.9, tile = 0.0168, two = 6.6, sum = 0.0288, round = 10.7; };
@@ -534,15 +538,15 @@ hipError_t launch_mx4_moment(Mx4MomentParams p, hipStream_t s) {
     return hipGetLastError();
   }
   // 256-tiles where there is enough to do for their longer start and end, and they fill their last round.
-  // Against 128-tiles: 65536 samples of 6400 features 694 and 798 us, 16384 of them 219 and 227, 65536 of 2560
-  // 134 and 146; 4096 features (136 tiles on 256 CUs) 350 and 320; 16384 of 2560 56 and 52.
+  // Against 128-tiles, from no cache: 65536 samples of 6400 features 657 and 762 us, 16384 of them 227 and 240, 65536
+  // of 2560 137 and 147; 4096 features (136 tiles on 256 CUs) 405 and 312; 16384 of 2560 62 and 50.
   const int nt = (p.dp + 255) / 256, tiles = nt * (nt + 1) / 2, left = tiles % kCUs;
   const bool fills = left == 0 || left * (kCUs / left) >= kCUs * 7 / 10;
   if (p.dp >= 2048 && fills && static_cast<int64_t>(stages) * tiles >= 6000)
     return launch_tiles<Cfg256>(p, cut_tiles<Cfg256>(p, stages), s);
   // 64-tiles have more CUs at work, and less to do at a tile's end; 128-tiles read half as much a product.  64 against
-  // 128 at its best, from no cache: 1024 samples of 1025 features 7.4 and 11.2 us, 4096 13.2 and 14.6, 4096 of 1600
-  // 16.5 and 19.5; 16384 of 1600 37 and 31, 4096 of 2560 27 and 23.4.
+  // 128 at its best, from no cache: 1024 samples of 1025 features 7.7 and 11.8 us, 4096 14.3 and 15.3, 4096 of 1600
+  // 17.0 and 20.1; 16384 of 1600 36 and 31, 4096 of 2560 26.4 and 23.9.
   const Cut small = cut_tiles<Cfg64>(p, stages), large = cut_tiles<Cfg128>(p, stages);
   return small.us < large.us ? launch_tiles<Cfg64>(p, small, s) : launch_tiles<Cfg128>(p, large, s);
 }
